@@ -1,7 +1,7 @@
 """Build libvq.so in-tree with nvcc for sm_100a (B200).
 
-The library is one translation unit, csrc/vq_api.cu, which includes every
-kernel. No GPU is needed to build; nvcc cross-compiles.
+The library is one translation unit, csrc/libvq.cu, which includes the block
+cache (vq_api.cu) and the paged cache (paged_api.cuh) with all their kernels. No GPU is needed to build; nvcc cross-compiles.
 """
 from __future__ import annotations
 
@@ -46,7 +46,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if not force and up_to_date():
         return LIB
     tmp = LIB + ".tmp"
-    cmd = [_nvcc(), *NVCC_FLAGS, "-I", os.path.join(ROOT, "include"), "-o", tmp, os.path.join(CSRC, "vq_api.cu")]
+    cmd = [_nvcc(), *NVCC_FLAGS, "-I", os.path.join(ROOT, "include"), "-o", tmp, os.path.join(CSRC, "libvq.cu")]
     if verbose:
         print(" ".join(cmd), file=sys.stderr)
     r = subprocess.run(cmd, capture_output=True, text=True)

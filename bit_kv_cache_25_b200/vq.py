@@ -17,7 +17,9 @@ import torch
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libvq.so")
 
 VQ_OK, VQ_ERR_INVALID_ARGUMENT, VQ_ERR_UNSUPPORTED, VQ_ERR_MISALIGNED, VQ_ERR_CUDA = range(5)
-VQ_BF16, VQ_F32 = 0, 1
+VQ_BF16, VQ_F32, VQ_F16 = 0, 1, 2
+VQ_INT8, VQ_E4M3 = 0, 1
+VQ_PAGE_TOKENS = 64
 
 
 class VqError(RuntimeError):
@@ -38,6 +40,25 @@ class vq_layer_cache(ctypes.Structure):
                 ("scale_v", ctypes.c_void_p), ("zero_v", ctypes.c_void_p)]
 
 
+class vq_paged_desc(ctypes.Structure):
+    _fields_ = [("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("code", ctypes.c_int32),
+                ("num_pages", ctypes.c_int32), ("max_pages", ctypes.c_int32)]
+
+
+class vq_paged_cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("pos", ctypes.c_void_p), ("weight", ctypes.c_void_p)]
+
+
+class vq_paged_query(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("q_heads", ctypes.c_int32), ("n", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("q", ctypes.c_void_p), ("q_strides", ctypes.c_int64 * 3),
+                ("block_table", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("q_lens", ctypes.c_void_p),
+                ("q_pos", ctypes.c_void_p), ("prefix", ctypes.c_void_p), ("first", ctypes.c_void_p),
+                ("slopes", ctypes.c_void_p), ("softmax_scale", ctypes.c_float), ("softcap", ctypes.c_float),
+                ("causal", ctypes.c_int32)]
+
+
 def _load():
     if not os.path.exists(_LIB_PATH):
         raise ImportError(f"{_LIB_PATH} is not built; run bit_kv_cache_25_b200.build.build() first")
@@ -55,6 +76,13 @@ def _load():
         "vq_paper_layout": [P(vq_cache_desc), P(SZ), P(SZ), P(SZ)],
         "vq_paper_pack": [P(vq_cache_desc), P(vq_layer_cache), VP, VP, VP, VP, VP],
         "vq_paper_unpack": [P(vq_cache_desc), VP, VP, VP, VP, P(vq_layer_cache), VP],
+        "vq_paged_append": [P(vq_paged_desc), P(vq_paged_cache), I32, I32, VP, VP, I32, I64P, I64P, VP, VP, VP, VP, VP],
+        "vq_paged_read": [P(vq_paged_desc), P(vq_paged_cache), I32, I32, VP, VP, VP, VP, VP, I32, I64P, I64P, VP],
+        "vq_paged_attention_workspace": [P(vq_paged_desc), I32, I32, I32, P(SZ)],
+        "vq_paged_attention": [P(vq_paged_desc), P(vq_paged_cache), P(vq_paged_query), VP, I64P, VP, VP, SZ, VP],
+        "vq_paged_weights": [P(vq_paged_desc), P(vq_paged_cache), P(vq_paged_query), VP, I32, VP],
+        "vq_paged_evict": [P(vq_paged_desc), P(vq_paged_cache), I32, VP, VP, P(vq_paged_desc), P(vq_paged_cache), VP, VP,
+                           I32, I32, I32, VP, VP],
         "vq_poll_device_error": [P(ctypes.c_uint32)],
         "vq_check_wait_timeout": [ctypes.c_uint32, VP],
         "vq_status_string": [I32],
@@ -72,6 +100,8 @@ _lib = _load()
 
 EXPORTED = ("vq_cache_layout", "vq_quantize_pack_block", "vq_cache_append", "vq_attention_block",
             "vq_append_attention_block", "vq_dequantize", "vq_paper_layout", "vq_paper_pack", "vq_paper_unpack",
+            "vq_paged_append", "vq_paged_read", "vq_paged_attention_workspace", "vq_paged_attention",
+            "vq_paged_weights", "vq_paged_evict",
             "vq_poll_device_error", "vq_check_wait_timeout", "vq_status_string", "vq_last_error", "vq_version")
 
 
@@ -327,6 +357,268 @@ def vq_dequantize(desc: CacheDesc, block: int, packed: torch.Tensor, scale: torc
     _check_devices(("packed", packed), ("scale", scale), ("zero", zero), ("out", out))
     _check(_lib.vq_dequantize(ctypes.byref(desc.c), block, packed.data_ptr(), scale.data_ptr(), zero.data_ptr(),
                               out.data_ptr(), _stream(stream)))
+
+
+# ---------------------------------------------------------------- paged 8-bit cache
+_CODES = {"int8": VQ_INT8, "e4m3": VQ_E4M3, VQ_INT8: VQ_INT8, VQ_E4M3: VQ_E4M3}
+_CODE_DTYPES = {VQ_INT8: (torch.int8, torch.uint8), VQ_E4M3: (torch.float8_e4m3fn, torch.uint8)}
+_PAGED_DTYPES = {torch.bfloat16: VQ_BF16, torch.float16: VQ_F16, torch.float32: VQ_F32}
+
+
+class PagedDesc:
+    """Shape of a paged cache: key heads, head_dim, "int8" or "e4m3" codes, pages in
+    the pools and pages in a row of the block table."""
+
+    def __init__(self, kv_heads: int, head_dim: int, code, num_pages: int, max_pages: int):
+        if code not in _CODES:
+            raise ValueError(f"code {code!r}: expected 'int8' or 'e4m3'")
+        self.kv_heads, self.head_dim, self.code = int(kv_heads), int(head_dim), _CODES[code]
+        self.num_pages, self.max_pages = int(num_pages), int(max_pages)
+        self.c = vq_paged_desc(self.kv_heads, self.head_dim, self.code, self.num_pages, self.max_pages)
+        self.ref = ctypes.byref(self.c)
+
+    def shape(self):
+        return (self.kv_heads, self.head_dim, self.code, self.num_pages, self.max_pages)
+
+
+class PagedCache:
+    """The pools of one layer: codes k, v [num_pages][kv_heads][64][head_dim], scales
+    [num_pages][kv_heads] and, if asked for, pos and weight [num_pages][kv_heads][64].
+    Given tensors are used as they are; the others are allocated here. The tensors of
+    a PagedCache stay the same for its life."""
+
+    def __init__(self, desc: PagedDesc, device="cuda", positions: bool = False, weights: bool = False, *, k=None,
+                 v=None, k_scale=None, v_scale=None, pos=None, weight=None):
+        n, h, d = desc.num_pages, desc.kv_heads, desc.head_dim
+        given = [t for t in (k, v, k_scale, v_scale, pos, weight) if t is not None]
+        if given:
+            device = given[0].device
+        slots = (n, h, VQ_PAGE_TOKENS)
+
+        def pool(name, t, shape, dtypes, want=True):
+            if t is None:
+                return torch.zeros(shape, dtype=dtypes[0], device=device) if want else None
+            if t.dtype not in dtypes:
+                raise ValueError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
+            if tuple(t.shape) != shape or not t.is_contiguous():
+                raise ValueError(f"{name} has shape {tuple(t.shape)}, expected contiguous {shape}")
+            if t.device != device:
+                raise ValueError(f"{name} is on {t.device}, the other tensors on {device}")
+            return t
+
+        codes = _CODE_DTYPES[desc.code]
+        self._desc = desc
+        self._k = pool("k", k, slots + (d,), codes)
+        self._v = pool("v", v, slots + (d,), codes)
+        self._k_scale = pool("k_scale", k_scale, (n, h), _F32)
+        self._v_scale = pool("v_scale", v_scale, (n, h), _F32)
+        self._pos = pool("pos", pos, slots, (torch.int32,), positions)
+        self._weight = pool("weight", weight, slots, _F32, weights)
+        self.device = self._k.device
+        self.c = vq_paged_cache(*(None if t is None else t.data_ptr() for t in
+                                  (self._k, self._v, self._k_scale, self._v_scale, self._pos, self._weight)))
+        self.ref = ctypes.byref(self.c)
+
+    desc = property(lambda self: self._desc)
+    k = property(lambda self: self._k)
+    v = property(lambda self: self._v)
+    k_scale = property(lambda self: self._k_scale)
+    v_scale = property(lambda self: self._v_scale)
+    pos = property(lambda self: self._pos)
+    weight = property(lambda self: self._weight)
+
+    def nbytes(self) -> int:
+        return sum(t.numel() * t.element_size() for t in
+                   (self._k, self._v, self._k_scale, self._v_scale, self._pos, self._weight) if t is not None)
+
+
+def _paged_cache_check(desc: PagedDesc, cache: PagedCache):
+    if cache.desc is not desc and cache.desc.shape() != desc.shape():
+        raise ValueError("the cache was made for another descriptor")
+    if cache.device.type != "cuda":
+        raise ValueError(f"the cache is on {cache.device}, not a CUDA device")
+    return cache.device
+
+
+def _array(name: str, t: Optional[torch.Tensor], shape, device, dtype=torch.int32, optional=True):
+    """Device address of a contiguous array argument; None if it is left out."""
+    if t is None:
+        if optional:
+            return None
+        raise ValueError(f"{name} is missing")
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} is {t.dtype} of shape {tuple(t.shape)}, expected contiguous {dtype} of {tuple(shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device} with the cache")
+    return t.data_ptr()
+
+
+def _view(name: str, t: torch.Tensor, shape, device):
+    """Strides of a [B][H][n][D] argument with channels contiguous."""
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    s = t.stride()
+    if s[3] != 1:
+        raise ValueError(f"{name}: the channel dimension must be contiguous")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device} with the cache")
+    return (ctypes.c_int64 * 3)(s[0], s[1], s[2])
+
+
+def _paged_dtype(name: str, t: torch.Tensor, allowed) -> int:
+    code = _PAGED_DTYPES.get(t.dtype)
+    if code not in allowed:
+        raise ValueError(f"{name} has unsupported dtype {t.dtype}")
+    return code
+
+
+def _rows(name: str, t: torch.Tensor, heads: Optional[int], desc: PagedDesc):
+    if t.dim() != 4:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [batch][heads][n][{desc.head_dim}]")
+    b, h, n, d = t.shape
+    if d != desc.head_dim or (heads is not None and h != heads):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [batch][{heads or 'heads'}][n][{desc.head_dim}]")
+    if b < 1 or n < 1:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}: batch and n must be at least 1")
+    return b, h, n
+
+
+def _on(device: torch.device, stream, call):
+    """Run call(stream handle) with `device` current, on `stream` or the device's current stream."""
+    if device.index is not None and device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return _on(device, stream, call)
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    _check(call(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)))
+
+
+def vq_paged_append(desc: PagedDesc, cache: PagedCache, block_table: torch.Tensor, start: torch.Tensor,
+                    k: torch.Tensor, v: torch.Tensor, counts: Optional[torch.Tensor] = None,
+                    pos: Optional[torch.Tensor] = None, stream=None):
+    """Quantize k, v [B][kv_heads][n][D] (bf16, fp16, fp32) into the sequences' pages as
+    tokens start[b] .. start[b] + counts[b] - 1 (counts None: n)."""
+    dev = _paged_cache_check(desc, cache)
+    B, _, n = _rows("k", k, desc.kv_heads, desc)
+    if k.dtype != v.dtype:
+        raise ValueError("k and v must have the same dtype")
+    dt = _paged_dtype("k", k, (VQ_BF16, VQ_F16, VQ_F32))
+    ks, vs = _view("k", k, k.shape, dev), _view("v", v, k.shape, dev)
+    table = _array("block_table", block_table, (B, desc.max_pages), dev, optional=False)
+    start = _array("start", start, (B,), dev, optional=False)
+    counts, pos = _array("counts", counts, (B,), dev), _array("pos", pos, (B,), dev)
+    _on(dev, stream, lambda s: _lib.vq_paged_append(desc.ref, cache.ref, B, n, k.data_ptr(), v.data_ptr(), dt, ks, vs,
+                                                    table, start, counts, pos, s))
+
+
+def vq_paged_read(desc: PagedDesc, cache: PagedCache, block_table: torch.Tensor, start: torch.Tensor,
+                  k_out: torch.Tensor, v_out: torch.Tensor, counts: Optional[torch.Tensor] = None, stream=None):
+    """Dequantize tokens start[b] .. start[b] + counts[b] - 1 into k_out, v_out [B][kv_heads][n][D]."""
+    dev = _paged_cache_check(desc, cache)
+    B, _, n = _rows("k_out", k_out, desc.kv_heads, desc)
+    if k_out.dtype != v_out.dtype:
+        raise ValueError("k_out and v_out must have the same dtype")
+    dt = _paged_dtype("k_out", k_out, (VQ_BF16, VQ_F16, VQ_F32))
+    ks, vs = _view("k_out", k_out, k_out.shape, dev), _view("v_out", v_out, k_out.shape, dev)
+    table = _array("block_table", block_table, (B, desc.max_pages), dev, optional=False)
+    start = _array("start", start, (B,), dev, optional=False)
+    counts = _array("counts", counts, (B,), dev)
+    _on(dev, stream, lambda s: _lib.vq_paged_read(desc.ref, cache.ref, B, n, table, start, counts, k_out.data_ptr(),
+                                                  v_out.data_ptr(), dt, ks, vs, s))
+
+
+def _paged_query(desc, block_table, lens, q, softmax_scale, q_lens, q_pos, prefix, first, slopes, softcap, causal, dev):
+    B, Hq, n = _rows("q", q, None, desc)
+    dt = _paged_dtype("q", q, (VQ_BF16, VQ_F16))
+    qs = _view("q", q, q.shape, dev)
+    return vq_paged_query(B, Hq, n, dt, q.data_ptr(), qs,
+                          _array("block_table", block_table, (B, desc.max_pages), dev, optional=False),
+                          _array("lens", lens, (B,), dev, optional=False), _array("q_lens", q_lens, (B,), dev),
+                          _array("q_pos", q_pos, (B,), dev), _array("prefix", prefix, (B,), dev),
+                          _array("first", first, (B, n), dev), _array("slopes", slopes, (Hq,), dev, torch.float32),
+                          softmax_scale, softcap, int(bool(causal)))
+
+
+def vq_paged_attention_workspace(desc: PagedDesc, batch: int, q_heads: int, n: int) -> int:
+    """Bytes of workspace that vq_paged_attention needs on the current device."""
+    size = ctypes.c_size_t()
+    _check(_lib.vq_paged_attention_workspace(desc.ref, batch, q_heads, n, ctypes.byref(size)))
+    return size.value
+
+
+def vq_paged_attention(desc: PagedDesc, cache: PagedCache, block_table: torch.Tensor, lens: torch.Tensor,
+                       q: torch.Tensor, softmax_scale: float, out: torch.Tensor, lse: Optional[torch.Tensor] = None, *,
+                       q_lens=None, q_pos=None, prefix=None, first=None, slopes=None, softcap: float = 0.0,
+                       causal: bool = False, workspace: Optional[torch.Tensor] = None, stream=None):
+    """Attention of q [B][Hq][n][D] (bf16 or fp16) over each sequence's first lens[b] cached
+    tokens, into out (q's shape and type) and lse [B][Hq][n] float32. The masks and biases are
+    vq.h's. workspace: a contiguous uint8 tensor of vq_paged_attention_workspace bytes that no
+    call running at the same time uses; None: allocated for this call."""
+    dev = _paged_cache_check(desc, cache)
+    query = _paged_query(desc, block_table, lens, q, softmax_scale, q_lens, q_pos, prefix, first, slopes, softcap,
+                         causal, dev)
+    if out.dtype != q.dtype:
+        raise ValueError(f"out is {out.dtype}, q is {q.dtype}: they must have the same dtype")
+    os_ = _view("out", out, q.shape, dev)
+    lse = _array("lse", lse, q.shape[:3], dev, torch.float32)
+    if workspace is not None:
+        if workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be contiguous on {dev}")
+
+    def call(s):
+        size = vq_paged_attention_workspace(desc, query.batch, query.q_heads, query.n)
+        ws = workspace
+        if ws is None and size:
+            # from the pool of the stream that the call runs on: memory goes back to it in its order
+            if stream is None:
+                ws = torch.empty(size, dtype=torch.uint8, device=dev)
+            else:
+                on = stream if hasattr(stream, "cuda_stream") else (
+                    torch.cuda.ExternalStream(int(stream), dev) if int(stream) else torch.cuda.default_stream(dev))
+                with torch.cuda.stream(on):
+                    ws = torch.empty(size, dtype=torch.uint8, device=dev)
+        ptr, have = (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
+        return _lib.vq_paged_attention(desc.ref, cache.ref, ctypes.byref(query), out.data_ptr(), os_, lse, ptr, have, s)
+
+    _on(dev, stream, call)
+
+
+def vq_paged_weights(desc: PagedDesc, cache: PagedCache, block_table: torch.Tensor, lens: torch.Tensor,
+                     q: torch.Tensor, softmax_scale: float, lse: torch.Tensor, *, q_lens=None, q_pos=None, prefix=None,
+                     first=None, slopes=None, softcap: float = 0.0, causal: bool = False, accumulate: bool = True,
+                     stream=None):
+    """Per cached token the sum of its attention weights over these queries (and the query heads
+    of its key head), added to cache.weight or put there; lse as vq_paged_attention gave it."""
+    dev = _paged_cache_check(desc, cache)
+    if cache.weight is None:
+        raise ValueError("the cache has no weight")
+    query = _paged_query(desc, block_table, lens, q, softmax_scale, q_lens, q_pos, prefix, first, slopes, softcap,
+                         causal, dev)
+    lse = _array("lse", lse, q.shape[:3], dev, torch.float32, optional=False)
+    _on(dev, stream, lambda s: _lib.vq_paged_weights(desc.ref, cache.ref, ctypes.byref(query), lse,
+                                                     int(bool(accumulate)), s))
+
+
+def vq_paged_evict(desc: PagedDesc, cache: PagedCache, block_table: torch.Tensor, lens: torch.Tensor,
+                   to_desc: PagedDesc, to: PagedCache, to_table: torch.Tensor, to_lens: torch.Tensor, keep: int, *,
+                   sinks: int = 0, recent: int = 0, kept: torch.Tensor, stream=None):
+    """Keep at most `keep` tokens per sequence and key head by cache.weight, moved in order to
+    the pages of to_table; writes to_lens [B] and the source slots kept [B][kv_heads][keep]."""
+    dev = _paged_cache_check(desc, cache)
+    if _paged_cache_check(to_desc, to) != dev:
+        raise ValueError(f"the caches are on {dev} and {to.device}")
+    if cache.weight is None:
+        raise ValueError("the cache has no weight")
+    if lens.dim() != 1 or lens.shape[0] < 1:
+        raise ValueError(f"lens has shape {tuple(lens.shape)}, expected [batch]")
+    B = lens.shape[0]
+    table = _array("block_table", block_table, (B, desc.max_pages), dev, optional=False)
+    lens = _array("lens", lens, (B,), dev, optional=False)
+    to_table = _array("to_table", to_table, (B, to_desc.max_pages), dev, optional=False)
+    to_lens = _array("to_lens", to_lens, (B,), dev, optional=False)
+    kept = _array("kept", kept, (B, desc.kv_heads, int(keep)), dev, optional=False)
+    _on(dev, stream, lambda s: _lib.vq_paged_evict(desc.ref, cache.ref, B, table, lens, to_desc.ref, to.ref, to_table,
+                                                   to_lens, int(keep), int(sinks), int(recent), kept, s))
 
 
 def vq_poll_device_error() -> int:

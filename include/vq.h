@@ -72,7 +72,7 @@ typedef enum {
   VQ_ERR_CUDA = 4              /* a CUDA runtime call or launch failed */
 } vq_status;
 
-typedef enum { VQ_BF16 = 0, VQ_F32 = 1 } vq_dtype;
+typedef enum { VQ_BF16 = 0, VQ_F32 = 1, VQ_F16 = 2 /* paged cache only */ } vq_dtype;
 
 /* Static description of one model's cache; lives on the host. */
 typedef struct {
@@ -205,11 +205,162 @@ vq_status vq_paper_unpack(const vq_cache_desc* desc, const uint32_t* k_words, co
 vq_status vq_dequantize(const vq_cache_desc* desc, int32_t block, const uint32_t* packed,
                         const float* scale, const float* zero, float* out, void* stream);
 
+/* ---- Paged 8-bit cache -------------------------------------------------------
+ *
+ * A cache that grows by any number of tokens per sequence, for decoding token by
+ * token or chunk by chunk: pages of VQ_PAGE_TOKENS tokens, each taken by one
+ * sequence through its row of a block table; codes of 8 bits with one float32
+ * scale per (page, key head) and tensor. A cached value is code * scale (one
+ * float32 product).
+ *
+ *   codes  [num_pages][kv_heads][64][head_dim] bytes, K and V each;
+ *   scales [num_pages][kv_heads] float32, K and V each;
+ *   pos    [num_pages][kv_heads][64] int32, a token's position, or NULL: its slot;
+ *   weight [num_pages][kv_heads][64] float32, a token's accumulated attention
+ *          weight, or NULL.
+ * Token j of sequence b is slot j: slot j % 64 of page block_table[b][j / 64].
+ *
+ * VQ_INT8: codes -127..127. A page first written with largest magnitude A has scale
+ *   max(A / 127, 2^-126) (A / 127 rounded to float32); x gets the nearest code of
+ *   the real quotient x / scale, ties to even.
+ * VQ_E4M3: codes are e4m3 numbers, the scale the smallest power of two (>= 2^-126)
+ *   with A <= 448 * scale; x gets the nearest e4m3 number to x / scale.
+ * A page is first written when its slot 0 is. Later tokens keep its scale while
+ * they fit (A < 127.5 * scale; A <= 448 * scale); else the scale grows by the
+ * smallest power of two that makes them fit, and the page's codes are rounded by
+ * it. A scale of 0 (only zeros so far) is replaced as a first write's.
+ * A NaN is stored as 0, magnitudes above 2^126 as 2^126.
+ *
+ * The conventions at the top of this file hold, with these additions:
+ *   - block_table, lens, start, counts, q_lens, q_pos, prefix, first (int32) and
+ *     slopes (float32) are device arrays aligned to 4 bytes; the pools, k, v, q, out,
+ *     lse and the workspace to 16.
+ *   - A length or page id out of range (a table entry below 0 or not below
+ *     num_pages where a token should be, a length above max_pages * 64) is never
+ *     followed: the access is skipped, its tokens count as unseen, and flag 4 is set
+ *     in the device error word (vq_poll_device_error). Table entries past a
+ *     sequence's last page are not read.
+ *   - What lies in a page behind its sequence's last token is never used, whatever
+ *     its bytes. Rows of padded queries (i >= q_lens[b]) are neither read nor
+ *     written.
+ *   - Two sequences of one append must not share a page that it writes; shared
+ *     pages may be read by any number.
+ *   - Results do not depend on the order in which blocks run: the same call on the
+ *     same inputs repeats to the bit.
+ *   - Supported: head_dim 64 or 128; any kv_heads; queries and outputs in bf16 or
+ *     fp16 (the output has the queries' type), new K/V in bf16, fp16 or float32. */
+#define VQ_PAGE_TOKENS 64
+
+typedef enum { VQ_INT8 = 0, VQ_E4M3 = 1 } vq_code;
+
+typedef struct {
+  int32_t kv_heads;  /* >= 1 */
+  int32_t head_dim;  /* 64 or 128 */
+  int32_t code;      /* vq_code */
+  int32_t num_pages; /* pages in the pools, >= 1 */
+  int32_t max_pages; /* entries of a row of the block table, >= 1 */
+} vq_paged_desc;
+
+/* The pools (device, caller-owned). */
+typedef struct {
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  int32_t* pos;  /* may be NULL */
+  float* weight; /* may be NULL */
+} vq_paged_cache;
+
+/* Quantize n new tokens of each of `batch` sequences into its pages: tokens
+ * start[b] .. start[b] + counts[b] - 1 (counts NULL: n for all). k, v: [batch]
+ * [kv_heads][n][head_dim] views (strides {batch, head, token}), rows past counts[b]
+ * not read. The pages must be in the block table already. Where the cache has them,
+ * the tokens' pos is written (pos[b] + t; pos NULL: the slot) and their weight set
+ * to 0. Lengths are the caller's: nothing here counts them up. */
+vq_status vq_paged_append(const vq_paged_desc* desc, const vq_paged_cache* cache, int32_t batch, int32_t n,
+                          const void* k, const void* v, vq_dtype dtype, const int64_t k_strides[3],
+                          const int64_t v_strides[3], const int32_t* block_table, const int32_t* start,
+                          const int32_t* counts, const int32_t* pos, void* stream);
+
+/* Dequantize tokens start[b] .. start[b] + counts[b] - 1 into k_out, v_out [batch]
+ * [kv_heads][n][head_dim], rounded to `dtype`. Rows past counts[b] are left as they
+ * are. The counterpart of vq_dequantize. */
+vq_status vq_paged_read(const vq_paged_desc* desc, const vq_paged_cache* cache, int32_t batch, int32_t n,
+                        const int32_t* block_table, const int32_t* start, const int32_t* counts, void* k_out,
+                        void* v_out, vq_dtype dtype, const int64_t k_strides[3], const int64_t v_strides[3],
+                        void* stream);
+
+/* The queries of an attention call and what each of them sees. Query i of
+ * sequence b (i < q_lens[b]) is the sequence's token lens[b] - q_lens[b] + i: its
+ * K and V are appended before the call. For query head hq (key head
+ * hq / (q_heads / kv_heads)), cached token j < lens[b] with position p_j:
+ *   z = softmax_scale * q . k_j;
+ *   softcap > 0:    z = softcap * tanh(z / softcap);
+ *   slopes:         z -= slopes[hq] * |p_query - p_j|, p_query = q_pos[b] + i
+ *                   (q_pos NULL: the query's slot);
+ *   seen if  (not causal, or j <= lens[b] - q_lens[b] + i, or p_j < prefix[b])
+ *        and (first NULL, or p_j >= first[b][i]).
+ * `first` is the first token of the query's document in a sequence of several, or
+ * the start of its window. After an eviction positions have gaps: pass q_pos. */
+typedef struct {
+  int32_t batch, q_heads, n;
+  vq_dtype dtype;             /* VQ_BF16 or VQ_F16, of q and out */
+  const void* q;              /* [batch][q_heads][n][head_dim] view */
+  int64_t q_strides[3];
+  const int32_t* block_table; /* [batch][max_pages] */
+  const int32_t* lens;        /* [batch] */
+  const int32_t* q_lens;      /* [batch] or NULL: n */
+  const int32_t* q_pos;       /* [batch] or NULL */
+  const int32_t* prefix;      /* [batch] or NULL: 0; only with causal */
+  const int32_t* first;       /* [batch][n] or NULL */
+  const float* slopes;        /* [q_heads] or NULL */
+  float softmax_scale;        /* (0, 1e6] */
+  float softcap;              /* 0 or (0, 1e6] */
+  int32_t causal;             /* 0 or 1 */
+} vq_paged_query;
+
+/* Bytes of workspace that vq_paged_attention needs on the current device for any
+ * call with this descriptor, batch, q_heads and n. Calls that can run at the same
+ * time need a workspace each. */
+vq_status vq_paged_attention_workspace(const vq_paged_desc* desc, int32_t batch, int32_t q_heads, int32_t n,
+                                       size_t* bytes);
+
+/* out[b][hq][i] = sum_j e^(z_j - lse) v_j over the tokens seen, lse = ln sum e^z_j
+ * ([batch][q_heads][n] float32, contiguous; may be NULL). A query that sees nothing
+ * gets 0 and -inf. */
+vq_status vq_paged_attention(const vq_paged_desc* desc, const vq_paged_cache* cache, const vq_paged_query* query,
+                             void* out, const int64_t out_strides[3], float* lse, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
+/* Per cached token and key head the sum of the weights e^(z_j - lse) over the
+ * call's queries and the query heads of that key head, with lse as
+ * vq_paged_attention gave it for the same query: added to cache->weight
+ * (accumulate 1) or put there (0), for tokens j < lens[b]. */
+vq_status vq_paged_weights(const vq_paged_desc* desc, const vq_paged_cache* cache, const vq_paged_query* query,
+                           const float* lse, int32_t accumulate, void* stream);
+
+/* Shrink sequences to at most `keep` tokens per key head, by accumulated weight:
+ * a sequence longer than keep keeps its first `sinks` and last `recent` tokens and,
+ * of the others, those of largest cache->weight (equal weights: the lowest slot; a
+ * NaN counts as -inf). The kept tokens go in order to slots 0 .. of the sequence's
+ * row of to_table in the pools `to` (pos and weight with them; without pos in
+ * `cache` the slot is the position), and to_lens[b] = min(lens[b], keep). kept
+ * [batch][kv_heads][keep] receives their source slots, -1 behind the last. A page's
+ * new scale is the largest of its tokens' old ones; a code of another scale is
+ * rounded once more. `to` may be the same pools, with pages that no sequence of
+ * `cache` that the call reads holds. keep >= 1, sinks + recent <= keep; to_desc has
+ * the same kv_heads, head_dim and code, and rows of at least keep / 64 pages. */
+vq_status vq_paged_evict(const vq_paged_desc* desc, const vq_paged_cache* cache, int32_t batch,
+                         const int32_t* block_table, const int32_t* lens, const vq_paged_desc* to_desc,
+                         const vq_paged_cache* to, const int32_t* to_table, int32_t* to_lens, int32_t keep,
+                         int32_t sinks, int32_t recent, int32_t* kept, void* stream);
+
 /* Read and clear the device error word of the current device. Kernels OR a
  * flag into it instead of trapping: 1 = a bounded wait on a shared-memory
  * barrier gave up (the affected outputs are not written), 2 = a kernel saw
- * parameters its launcher should have rejected. Synchronizes with the device
- * (a blocking copy). */
+ * parameters its launcher should have rejected, 4 = a call on a paged cache met
+ * a length or a page id out of range and skipped that access. Synchronizes with
+ * the device (a blocking copy). */
 vq_status vq_poll_device_error(uint32_t* code);
 
 /* Self-test of the device error path (no counterpart on the pages; it checks
