@@ -5,8 +5,8 @@
 #pragma once
 
 #include "paged.cuh"
-#include "paged_attention.cuh"
 #include "paged_evict.cuh"
+#include "paged_launch.cuh"
 
 namespace {
 
