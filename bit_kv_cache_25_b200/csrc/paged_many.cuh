@@ -3,14 +3,14 @@
 //
 // A work item is up to 256 rows (two tiles of 128, row r = i * G + g as in
 // paged_attention.cuh) of one (sequence, key head) against its pages, 128 keys
-// (two pages) at a time. One CTA per item and SM, 13 warps:
+// (two pages) at a time. One CTA per item and SM:
 //   - two softmax warpgroups, one thread per row: query rows to shared memory
 //     (bf16 rows times a power of two, exact in fp16), then per key tile the row
 //     maximum, 2^(z - R + 7) as fp16 over the scores' own columns, and at the end
 //     the output;
-//   - four unpack warps: codes straight from global memory into registers one
-//     tile ahead, converted (exactly) to fp16 and stored as swizzled K-major
-//     tiles, which serve K as they are and V read MN-major;
+//   - four warps unpack K and three V: codes straight from global memory into
+//     registers one tile ahead, converted (exactly) to fp16 and stored as swizzled
+//     K-major tiles, which serve K as they are and V read MN-major;
 //   - one MMA warp: S = Q K^T, O += P V (P from tensor memory), ordered so that one
 //     tile's products run while the other's softmax does.
 // The scales stay out of the operands: K's is a factor of the scores, V's goes into the
@@ -50,10 +50,76 @@ struct ManyCfg {
   static constexpr int V0_SLOT = TMEM_SLOT + 8;
   static constexpr int SMEM = V0_SLOT + 8;
   static constexpr int SMEM_ALLOC = SMEM + 1024;
-  static constexpr int THREADS = 13 * 32;
+  static constexpr int THREADS = 512;  // 128 registers each at launch, shared out below: 256 x 168 + 128 x 80 + 128 x 96
   static constexpr int COL_O = 128;  // tile qt: columns 256 * qt: scores [0, 128), output [128, 128 + D)
   static_assert(SMEM_ALLOC <= 232448 && TILE % 1024 == 0, "shared memory");
 };
+
+// Thread t of the warp reads TMEM lane (base + t), 32 consecutive 32-bit columns; not waited for.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* x) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+#pragma unroll
+  for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(r[i]);
+}
+
+// One arrival for the whole warp, after all of its lanes' work.
+__device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
+}
+
+// The registers of this warpgroup's threads from here on.
+template <int N>
+__device__ __forceinline__ void set_registers() {
+  if constexpr (N > 128)
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+  else
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// (page * H + h) of pages index and index + 1 of sequence b; -1 where no token is, or the page id is out of range.
+__device__ __forceinline__ void many_pages(const PagedAttnParams& p, const SeqView& sv, int b, int h, int index,
+                                           int64_t (&ph)[2]) {
+  const int last = (sv.len + kPage - 1) / kPage;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int page = index + i < last ? paged_page(p.c, b, index + i) : -1;
+    ph[i] = page < 0 ? -1 : static_cast<int64_t>(page) * p.c.H + h;
+  }
+}
+
+// Which row (of the warp load's 128 / D * 4) and which 16 codes of it a lane takes: a quarter of the warp takes 64
+// channels of two rows, so that its 16-byte stores cover all banks (chunks 0, 2, 4, 6 of one row and 1, 3, 5, 7 of
+// the next, under the swizzle).
+template <int D>
+__device__ __forceinline__ void unpack_lane(int lane, int& row, int& g) {
+  const int quarter = lane >> 3;
+  row = (D == 128 ? (quarter >> 1) * 2 : quarter * 2) + ((lane >> 2) & 1);
+  g = (D == 128 ? (quarter & 1) * 4 : 0) + (lane & 3);
+}
+// Byte offset of row `row`, 16-code group g in the K-major 128-byte-swizzled fp16 tile of 128 rows: its first 16
+// bytes; the other 16 are at the offset xor 16.
+__device__ __forceinline__ uint32_t unpack_at(int row, int g) {
+  return (g >> 2) * (128 * 128) + (row >> 3) * 1024 + (row & 7) * 128 + ((((g & 3) * 2) ^ (row & 7)) << 4);
+}
+template <int CODE>
+__device__ __forceinline__ void store_codes(const uint4& x, uint32_t at) {
+  uint32_t y[8];
+  codes_f16<CODE>(x.x, y[0], y[1]);
+  codes_f16<CODE>(x.y, y[2], y[3]);
+  codes_f16<CODE>(x.z, y[4], y[5]);
+  codes_f16<CODE>(x.w, y[6], y[7]);
+  tc::sts128(at, y[0], y[1], y[2], y[3]);
+  tc::sts128(at ^ 16u, y[4], y[5], y[6], y[7]);
+}
 
 struct ManyRow {
   int lo, hi;   // slots seen (general mode: hi is the causal bound, lo unused)
@@ -93,19 +159,19 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1) paged_many_kernel(cons
   const int nq = rows - row0 > 128 ? 2 : 1;
 
   // ---- set-up
-  if (warp == 12) {
+  if (warp == 15) {
     tc::tmem_alloc(tmem_slot, 512);
     tc::tmem_relinquish();
   }
   if (tid == 0) {
-    mbar_init(q_full, nq * 128);
+    mbar_init(q_full, nq * 4);  // (one arrival per warp)
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&k_full[i], 128);
-      mbar_init(&v_full[i], 128);
+      mbar_init(&k_full[i], 4);
+      mbar_init(&v_full[i], 3);
       mbar_init(&k_empty[i], 1);
       mbar_init(&v_empty[i], 1);
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 128);
+      mbar_init(&p_full[i], 4);
     }
     mbar_init(o_full, 1);
     fence_barrier_init();
@@ -160,6 +226,7 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1) paged_many_kernel(cons
     // nothing to see: the rows are written below
   } else if (warp < 8) {
     // ================================================================ softmax
+    set_registers<168>();
     const int qt = warp >> 2;
     if (qt < nq) {
       const uint32_t lane_tm = tm + (static_cast<uint32_t>((warp & 3) * 32) << 16) + qt * 256;
@@ -197,7 +264,7 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1) paged_many_kernel(cons
           tc::sts128(at + (c >> 3) * (128 * 128) + (((c & 7) ^ (r & 7)) << 4), v[c].x, v[c].y, v[c].z, v[c].w);
         }
         fence_proxy_async_smem();
-        mbar_arrive(q_full);
+        warp_arrive(q_full, lane);
       }
       const float fz = p.sigma * back * (MODE == kManyPlain ? kLog2e : 1.0f);
       const float cap_f = MODE != kManyPlain && p.cap > 0.0f ? 2.0f * kLog2e / p.cap : 0.0f;
@@ -231,143 +298,112 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1) paged_many_kernel(cons
           }
           return z;
         };
-        float top[2];
+        float xs[2][64];
+        tmem_ld32(lane_tm, xs[0]);
+        tmem_ld32(lane_tm + 32, xs[0] + 32);
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          float m = -INFINITY;
-#pragma unroll 1
-          for (int ch = 0; ch < 2; ++ch) {
-            uint32_t a[2][16];
-            const int c0 = half * 64 + ch * 32;
-            tc::tmem_ld16(lane_tm + c0, a[0]);
-            tc::tmem_ld16(lane_tm + c0 + 16, a[1]);
-            tc::tmem_wait_ld();
-            float x[32];
+        for (int half = 0; half < 2; ++half) {  // one page: its scores stay in registers
+          const int c0 = half * 64;
+          const float f = half ? f1 : f0, lc = hdr[2 + half];
+          float(&x)[64] = xs[half];
+          tc::tmem_wait_ld();
+          if (MODE != kManyPlain) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              x[i] = __uint_as_float(a[i >> 4][i & 15]);
-              if (MODE == kManyGeneral) x[i] = score(x[i], half ? f1 : f0, c0 + i);
-              if (!whole && !seen(c0 + i)) x[i] = -INFINITY;
-            }
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) m = tc::max3(m, x[i], x[i + 1]);
+            for (int i = 0; i < 64; ++i) x[i] = score(x[i], f, c0 + i);
           }
-          // scores grow with the raw products where no bias depends on the key
-          if (MODE != kManyGeneral && m > -INFINITY) m = score(m, half ? f1 : f0, 0);
-          top[half] = m + hdr[2 + half];
-        }
-        __syncwarp();
-        const float t = fmaxf(top[0], top[1]);
-        const bool move = t > R + 8.0f;
-        if (__any_sync(0xffffffffu, move)) {
-          const float g = move ? tc::ex2(R - t) : 1.0f;
-          if (move) R = t;
-          l *= g;
-          if (j > 0) {
-#pragma unroll 1
-            for (int c = 0; c < D; c += 16) {
-              uint32_t o[16];
-              tc::tmem_ld16(lane_tm + C::COL_O + c, o);
-              tc::tmem_wait_ld();
+          if (!whole) {
 #pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * g);
-              tc::tmem_st16(lane_tm + C::COL_O + c, o);
-            }
-            tc::tmem_wait_st();
+            for (int i = 0; i < 64; ++i) x[i] = seen(c0 + i) ? x[i] : -INFINITY;
           }
-        }
-        const float base = (R == -INFINITY ? 0.0f : R) - 7.0f;
+          float mx[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const float f = half ? f1 : f0, off = hdr[2 + half] - base;
+          for (int i = 4; i < 60; i += 8)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mx[k] = tc::max3(mx[k], x[i + 2 * k], x[i + 2 * k + 1]);
+          const float m = tc::max3(tc::max3(mx[0], x[60], x[61]), tc::max3(mx[1], x[62], x[63]), fmaxf(mx[2], mx[3]));
+          const float t = MODE == kManyPlain ? fmaf(m, f, lc) : m + lc;
+          const bool move = t > R + 8.0f;
+          if (__any_sync(0xffffffffu, move)) {
+            const float g = move ? tc::ex2(R - t) : 1.0f;
+            if (move) R = t;
+            l *= g;
+            __syncwarp();
+            if (half) {  // the first page's weights of this tile
+#pragma unroll 1
+              for (int c = 0; c < 32; c += 16) {
+                uint32_t w[16];
+                tc::tmem_ld16(lane_tm + c, w);
+                tc::tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                  const float2 v = __half22float2(*reinterpret_cast<__half2*>(&w[i]));
+                  w[i] = tc::cvt_half2(v.x * g, v.y * g);
+                }
+                tc::tmem_st16(lane_tm + c, w);
+              }
+            }
+            if (j > 0) {
+#pragma unroll 1
+              for (int c = 0; c < D; c += 16) {
+                uint32_t o[16];
+                tc::tmem_ld16(lane_tm + C::COL_O + c, o);
+                tc::tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * g);
+                tc::tmem_st16(lane_tm + C::COL_O + c, o);
+              }
+            }
+          }
+          const float off = lc - (R == -INFINITY ? 0.0f : R) + 7.0f;
           uint64_t sum2 = 0;
-#pragma unroll 1
-          for (int ch = 0; ch < 2; ++ch) {
-            uint32_t a[2][16], w[16];
-            const int c0 = half * 64 + ch * 32;
-            tc::tmem_ld16(lane_tm + c0, a[0]);
-            tc::tmem_ld16(lane_tm + c0 + 16, a[1]);
-            tc::tmem_wait_ld();
+#pragma unroll
+          for (int ch = 0; ch < 64; ch += 32) {
+            uint32_t w[16];
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {
-              float x0 = __uint_as_float(a[i >> 4][i & 15]), x1 = __uint_as_float(a[i >> 4][(i & 15) + 1]);
-              if (MODE == kManyPlain) {
-                if (!whole) {
-                  x0 = seen(c0 + i) ? x0 : -INFINITY;
-                  x1 = seen(c0 + i + 1) ? x1 : -INFINITY;
-                }
-                const uint64_t z = tc::fma2(tc::f2pack(x0, x1), tc::f2pack(f, f), tc::f2pack(off, off));
-                x0 = tc::f2lo(z);
-                x1 = tc::f2hi(z);
-              } else {
-                x0 = score(x0, f, c0 + i) + off;
-                x1 = score(x1, f, c0 + i + 1) + off;
-                if (!whole) {
-                  x0 = seen(c0 + i) ? x0 : -INFINITY;
-                  x1 = seen(c0 + i + 1) ? x1 : -INFINITY;
-                }
-              }
-              const float p0 = tc::ex2(x0), p1 = tc::ex2(x1);
+              const uint64_t y = tc::f2pack(x[ch + i], x[ch + i + 1]);
+              const uint64_t z = MODE == kManyPlain ? tc::fma2(y, tc::f2pack(f, f), tc::f2pack(off, off))
+                                                    : tc::add2(y, tc::f2pack(off, off));
+              const float p0 = tc::ex2(tc::f2lo(z)), p1 = tc::ex2(tc::f2hi(z));
               sum2 = tc::add2(sum2, tc::f2pack(p0, p1));
               w[i >> 1] = tc::cvt_half2(p0, p1);
             }
             // over columns whose scores this row has read
-            tc::tmem_st16(lane_tm + half * 32 + ch * 16, w);
+            tc::tmem_st16(lane_tm + half * 32 + ch / 2, w);
+            if (half == 0) tmem_ld32(lane_tm + 64 + ch, xs[1] + ch);  // the next page's, while these are worked on
           }
           l = fmaf(tc::f2lo(sum2) + tc::f2hi(sum2), hdr[4 + half], l);
         }
         tc::tmem_wait_st();
         tc::fence_before_sync();
-        mbar_arrive(&p_full[qt]);
+        warp_arrive(&p_full[qt], lane);
       }
     }
   } else if (warp < 12) {
-    // ================================================================= unpack
-    constexpr int G = D / 16, N = D / 16, RPI = 128 / G;  // 16-code groups per row, loads per thread, rows per load
+    // =============================================================== unpack K
+    set_registers<80>();
+    constexpr int RPW = 512 / D, N = 128 / RPW / 4, STEP = 4 * RPW;  // rows per warp load, loads per lane, rows between them
     const int u = tid - 256;
-    const int g = u % G, r0 = u / G;
-    const int last = (sv.len + kPage - 1) / kPage;  // pages that hold tokens
-    uint4 kr[N], vr[N];
-    int64_t ph[2];     // (page * H + h) of the tile's two pages, -1: none
+    int r0, g;
+    unpack_lane<D>(lane, r0, g);
+    r0 += (warp - 8) * RPW;
+    const uint32_t to = sbase + C::K0 + unpack_at(r0, g);  // (STEP rows are whole groups of 8: a constant further on)
+    const int from = r0 * D + g * 16;
+    uint4 x[N];
+    int64_t ph[2];
     float ks[2], vs[2];
     int pos = 0;
     float v0 = 0.0f;
-    auto locate = [&](int j) {
+    auto load = [&](int j) {
+      many_pages(p, sv, b, h, (t0 + j) * 2, ph);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int index = (t0 + j) * 2 + i;
-        const int page = index < last ? paged_page(p.c, b, index) : -1;
-        ph[i] = page < 0 ? -1 : static_cast<int64_t>(page) * p.c.H + h;
-      }
-    };
-    auto load = [&](const unsigned char* code, const int64_t (&at)[2], uint4 (&x)[N]) {
+      for (int half = 0; half < 2; ++half) {
+        const unsigned char* src = p.c.code[0] + ph[half] * (kPage * D) + from;
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const int row = (i * RPI + r0) & 63;
-        const int64_t a = at[i >= N / 2];
-        x[i] = a < 0 ? make_uint4(0, 0, 0, 0) : __ldg(reinterpret_cast<const uint4*>(code + (a * kPage + row) * D + g * 16));
+        for (int i = 0; i < N / 2; ++i)
+          x[half * (N / 2) + i] =
+              ph[half] < 0 ? make_uint4(0, 0, 0, 0) : __ldg(reinterpret_cast<const uint4*>(src + i * STEP * D));
       }
-    };
-    auto store = [&](const uint4 (&x)[N], uint32_t dst) {
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const int row = i * RPI + r0;
-        const uint32_t at = dst + (g >> 2) * (128 * 128) + (row >> 3) * 1024 + (row & 7) * 128;
-        uint32_t y[8];
-        codes_f16<CODE>(x[i].x, y[0], y[1]);
-        codes_f16<CODE>(x[i].y, y[2], y[3]);
-        codes_f16<CODE>(x[i].z, y[4], y[5]);
-        codes_f16<CODE>(x[i].w, y[6], y[7]);
-        const uint32_t c0 = (g & 3) * 2;
-        // (the second 64 channels' lanes store their odd chunk first: eight lanes then cover all banks)
-        const bool odd = (g >> 2) & 1;
-        tc::sts128(at + (((c0 + odd) ^ (row & 7)) << 4), odd ? y[4] : y[0], odd ? y[5] : y[1], odd ? y[6] : y[2],
-                   odd ? y[7] : y[3]);
-        tc::sts128(at + (((c0 + 1 - odd) ^ (row & 7)) << 4), odd ? y[0] : y[4], odd ? y[1] : y[5], odd ? y[2] : y[6],
-                   odd ? y[3] : y[7]);
-      }
-    };
-    auto scales = [&]() {
       if (u == 0) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -377,13 +413,11 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1) paged_many_kernel(cons
       }
       if (MODE == kManyGeneral && p.c.pos) pos = ph[u >> 6] < 0 ? 0 : __ldg(p.c.pos + ph[u >> 6] * kPage + (u & 63));
     };
-    locate(0);
-    scales();
-    load(p.c.code[0], ph, kr);
-    load(p.c.code[1], ph, vr);
+    load(0);
     for (int j = 0; j < T; ++j) {
       if (j >= 2 && !(ok = mbar_wait_warp(&k_empty[j & 1], ((j >> 1) - 1) & 1))) break;
-      store(kr, sbase + C::K0 + (j & 1) * C::TILE);
+#pragma unroll
+      for (int i = 0; i < N; ++i) store_codes<CODE>(x[i], to + (j & 1) * C::TILE + i * STEP * 128);
       // header of the tile; its slot was last read by the softmax of tile j - 4, which tile j - 2's products follow
       float* hdr = reinterpret_cast<float*>(sm + C::HDR0 + (j & 3) * C::HDR);
       if (u == 0) {
@@ -405,20 +439,48 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1) paged_many_kernel(cons
       }
       if (MODE == kManyGeneral && p.c.pos) reinterpret_cast<int*>(hdr + 8)[u] = pos;
       fence_proxy_async_smem();
-      mbar_arrive(&k_full[j & 1]);
-      if (j + 1 < T) {
-        locate(j + 1);
-        scales();
-        load(p.c.code[0], ph, kr);
+      warp_arrive(&k_full[j & 1], lane);
+      if (j + 1 < T) load(j + 1);
+    }
+  } else if (warp < 15) {
+    // =============================================================== unpack V
+    set_registers<96>();
+    // the three warps take the tile's warp loads (RPW rows each) in turn
+    constexpr int RPW = 512 / D, LOADS = 128 / RPW, N = (LOADS + 2) / 3;
+    int r0, g;
+    unpack_lane<D>(lane, r0, g);
+    const int w = warp - 12;
+    const int from = r0 * D + g * 16;
+    uint4 x[N];
+    int64_t ph[2];
+    auto load = [&](int j) {
+      many_pages(p, sv, b, h, (t0 + j) * 2, ph);
+      const unsigned char* src0 = p.c.code[1] + ph[0] * (kPage * D) + from;
+      const unsigned char* src1 = p.c.code[1] + (ph[1] - 1) * (kPage * D) + from;  // rows 64 .. 127
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int q = 3 * i + w;  // (warp-uniform)
+        const bool late = q >= LOADS / 2;
+        x[i] = make_uint4(0, 0, 0, 0);
+        if (q < LOADS && ph[late] >= 0) x[i] = __ldg(reinterpret_cast<const uint4*>((late ? src1 : src0) + q * (RPW * D)));
       }
+    };
+    load(0);
+    for (int j = 0; j < T; ++j) {
       if (j >= 2 && !(ok = mbar_wait_warp(&v_empty[j & 1], ((j >> 1) - 1) & 1))) break;
-      store(vr, sbase + C::V0 + (j & 1) * C::TILE);
+      const uint32_t to = sbase + C::V0 + (j & 1) * C::TILE;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int q = 3 * i + w;
+        if (q < LOADS) store_codes<CODE>(x[i], to + unpack_at(q * RPW + r0, g));
+      }
       fence_proxy_async_smem();
-      mbar_arrive(&v_full[j & 1]);
-      if (j + 1 < T) load(p.c.code[1], ph, vr);
+      warp_arrive(&v_full[j & 1], lane);
+      if (j + 1 < T) load(j + 1);
     }
   } else {
     // ==================================================================== MMA
+    set_registers<96>();
     const uint32_t idesc_qk = tc::idesc_f16_f32(128, 128);
     const uint32_t idesc_pv = tc::idesc_f16_f32(128, D, /*b_mn_major=*/true);
     const uint64_t qd = tc::sw128_desc(sbase + C::Q0);
@@ -521,7 +583,7 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1) paged_many_kernel(cons
     tc::fence_before_sync();
   }
   __syncthreads();
-  if (warp == 12) {
+  if (warp == 15) {
     tc::fence_after_sync();
     tc::tmem_dealloc(tm, 512);
   }
