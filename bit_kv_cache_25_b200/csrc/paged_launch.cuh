@@ -3,6 +3,7 @@
 
 #include "paged_attention.cuh"
 #include "paged_many.cuh"
+#include "paged_weights.cuh"
 
 namespace vq {
 
@@ -73,6 +74,10 @@ inline cudaError_t launch_paged_attention(PagedAttnParams& p, const PagedPlan& p
 
 inline cudaError_t launch_paged_weights(PagedAttnParams& p, int code, cudaStream_t stream) {
   const int64_t grid = static_cast<int64_t>(p.B) * p.c.H * ((p.c.max_pages + 1) / 2);
+  if (static_cast<int64_t>(p.n) * p.G > kFewRows)
+    return many_dispatch(p, code, [&](auto d, auto c, auto m) {
+      return launch_sums_variant<d(), c(), m()>(p, static_cast<unsigned>(grid), stream);
+    });
   return paged_attn_dispatch(p.c.D, code, paged_biased(p), [&](auto d, auto c, auto bias) {
     paged_weights_kernel<d(), c(), bias()><<<static_cast<unsigned>(grid), kFewWarps * 32, 0, stream>>>(p);
     return cudaGetLastError();

@@ -45,7 +45,7 @@ struct ManyCfg {
   static constexpr int HDR0 = V0 + 2 * TILE;  // 4 x {8 floats, 128 positions}
   static constexpr int HDR = 32 + 128 * 4;
   static constexpr int BARS = HDR0 + 4 * HDR;
-  static constexpr int NBARS = 14;
+  static constexpr int NBARS = 18;
   static constexpr int TMEM_SLOT = BARS + NBARS * 8;
   static constexpr int V0_SLOT = TMEM_SLOT + 8;
   static constexpr int SMEM = V0_SLOT + 8;
@@ -143,6 +143,7 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1) paged_many_kernel(cons
   uint64_t* s_full = q_full + 9;
   uint64_t* p_full = q_full + 11;
   uint64_t* o_full = q_full + 13;
+  uint64_t* h_full = q_full + 14;  // four headers
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + C::TMEM_SLOT);
   float* v0_slot = reinterpret_cast<float*>(sm + C::V0_SLOT);
   __shared__ int range[2];  // slots that any row of the item sees
@@ -174,6 +175,7 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1) paged_many_kernel(cons
       mbar_init(&p_full[i], 4);
     }
     mbar_init(o_full, 1);
+    for (int i = 0; i < 4; ++i) mbar_init(&h_full[i], 4);
     fence_barrier_init();
     range[0] = INT32_MAX;
     range[1] = 0;
@@ -270,7 +272,7 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1) paged_many_kernel(cons
       const float cap_f = MODE != kManyPlain && p.cap > 0.0f ? 2.0f * kLog2e / p.cap : 0.0f;
       for (int j = 0; j < T; ++j) {
         const int slot0 = (t0 + j) * C::KT;
-        ok = mbar_wait_warp(&k_full[j & 1], (j >> 1) & 1) && mbar_wait_warp(&s_full[qt], j & 1);
+        ok = mbar_wait_warp(&h_full[j & 3], (j >> 2) & 1) && mbar_wait_warp(&s_full[qt], j & 1);
         if (!ok) break;
         tc::fence_after_sync();
         const float* hdr = reinterpret_cast<const float*>(sm + C::HDR0 + (j & 3) * C::HDR);
@@ -440,6 +442,7 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1) paged_many_kernel(cons
       if (MODE == kManyGeneral && p.c.pos) reinterpret_cast<int*>(hdr + 8)[u] = pos;
       fence_proxy_async_smem();
       warp_arrive(&k_full[j & 1], lane);
+      if (lane == 0) mbar_arrive(&h_full[j & 3]);
       if (j + 1 < T) load(j + 1);
     }
   } else if (warp < 15) {
@@ -606,18 +609,24 @@ cudaError_t launch_many_variant(const PagedAttnParams& p, unsigned grid, cudaStr
   return cudaGetLastError();
 }
 
-inline cudaError_t launch_paged_many(const PagedAttnParams& p, int code, unsigned grid, cudaStream_t stream) {
+// f(head_dim tag, code tag, mode tag) for the call's variant.
+template <typename F>
+cudaError_t many_dispatch(const PagedAttnParams& p, int code, F f) {
   const bool general = p.slopes || (p.c.pos && (p.first || (p.prefix && p.causal)));
   auto by_mode = [&](auto d, auto c) {
-    if (general) return launch_many_variant<d(), c(), kManyGeneral>(p, grid, stream);
-    if (p.cap > 0.0f) return launch_many_variant<d(), c(), kManyCap>(p, grid, stream);
-    return launch_many_variant<d(), c(), kManyPlain>(p, grid, stream);
+    if (general) return f(d, c, std::integral_constant<int, kManyGeneral>{});
+    if (p.cap > 0.0f) return f(d, c, std::integral_constant<int, kManyCap>{});
+    return f(d, c, std::integral_constant<int, kManyPlain>{});
   };
   auto by_code = [&](auto d) {
     return code == kCodeInt8 ? by_mode(d, std::integral_constant<int, kCodeInt8>{})
                              : by_mode(d, std::integral_constant<int, kCodeE4m3>{});
   };
   return p.c.D == 64 ? by_code(std::integral_constant<int, 64>{}) : by_code(std::integral_constant<int, 128>{});
+}
+
+inline cudaError_t launch_paged_many(const PagedAttnParams& p, int code, unsigned grid, cudaStream_t stream) {
+  return many_dispatch(p, code, [&](auto d, auto c, auto m) { return launch_many_variant<d(), c(), m()>(p, grid, stream); });
 }
 
 }  // namespace
