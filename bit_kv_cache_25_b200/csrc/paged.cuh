@@ -71,7 +71,7 @@ __device__ __forceinline__ int paged_len(const PagedPool& p, const int32_t* lens
 }
 
 // ---- codes
-// Two int8 codes (bytes 0, 1 of `pair`, each xor 0x80) as fp16x2: the byte u = code
+// Two int8 codes (each xor 0x80; `sel` picks their bytes) as fp16x2: the byte u = code
 // + 128 under the high byte 0x64 is the fp16 number 1024 + u, exactly.
 __device__ __forceinline__ uint32_t int8_pair_f16(uint32_t flipped, uint32_t sel) {
   const uint32_t v = __byte_perm(flipped, 0x64646464u, sel);
@@ -95,6 +95,18 @@ __device__ __forceinline__ void codes_f16(uint32_t w, uint32_t& lo, uint32_t& hi
   } else {
     lo = e4m3_pair_f16(w, 0x1404);
     hi = e4m3_pair_f16(w, 0x3424);
+  }
+}
+// The four codes of a word that holds two channels (bytes 0, 1 and 2, 3) of two tokens: channel 0 of both, channel 1.
+template <int CODE>
+__device__ __forceinline__ void codes_f16_of_two(uint32_t w, uint32_t& even, uint32_t& odd) {
+  if (CODE == kCodeInt8) {
+    w ^= 0x80808080u;
+    even = int8_pair_f16(w, 0x4240);
+    odd = int8_pair_f16(w, 0x4341);
+  } else {
+    even = e4m3_pair_f16(w, 0x2404);
+    odd = e4m3_pair_f16(w, 0x3414);
   }
 }
 // What codes_f16 leaves to the scale.

@@ -256,7 +256,7 @@ vq_status vq_paged_attention(const vq_paged_desc* desc, const vq_paged_cache* ca
   if (need > workspace_bytes || (need && !workspace))
     return fail(VQ_ERR_INVALID_ARGUMENT, "workspace of %zu bytes, %zu needed", workspace ? workspace_bytes : 0, need);
   if ((st = check_grid(int64_t(p.B) * p.c.H * plan.row_tiles * plan.splits)) != VQ_OK) return st;
-  if ((st = check_grid((int64_t(p.B) * p.Hq * p.n + 3) / 4)) != VQ_OK) return st;
+  if ((st = check_grid(int64_t(p.B) * p.Hq * p.n)) != VQ_OK) return st;
   e = vq::launch_paged_attention(p, plan, desc->code, workspace, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "paged attention launch");
   return ok();
@@ -273,7 +273,10 @@ vq_status vq_paged_weights(const vq_paged_desc* desc, const vq_paged_cache* cach
   p.lse = const_cast<float*>(lse);
   p.accumulate = accumulate;
   if ((st = check_grid(int64_t(p.B) * p.c.H * ((p.c.max_pages + 1) / 2))) != VQ_OK) return st;
-  cudaError_t e = vq::launch_paged_weights(p, desc->code, static_cast<cudaStream_t>(stream));
+  int sms = 0;
+  cudaError_t e = paged_sms(&sms);
+  if (e != cudaSuccess) return cuda_fail(e, "reading the device's size");
+  e = vq::launch_paged_weights(p, desc->code, sms, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "paged weights launch");
   return ok();
 }

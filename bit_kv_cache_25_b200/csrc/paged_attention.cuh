@@ -20,6 +20,7 @@
 #include <type_traits>
 
 #include "paged.cuh"
+#include "vq_internal.h"
 
 namespace vq {
 
@@ -56,6 +57,13 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4],
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// The first product of a sum.
+__device__ __forceinline__ void mma_16816_from_zero(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
 // cap * tanh(z / cap), times log2 e. tanh(x) = 1 - 2 / (e^2x + 1): its error is a few
@@ -104,13 +112,24 @@ __device__ __forceinline__ RowView row_view(const PagedAttnParams& p, const SeqV
   return v;
 }
 
-// The A fragments of 16 query rows (rows r and r + 8 of lane 4r + c): channel order
-// as in the K loads below. Rows past the call's are zero and not read. bf16 rows are
-// multiplied by a power of two that puts their largest magnitude in [2^7, 2^8); `back`
-// undoes it.
+// What the scores need beyond the product: nothing but an interval of slots per row; a cap too; or terms that
+// depend on positions.
+enum PagedMode : int { kPlain = 0, kCap = 1, kGeneral = 2 };
+
+// A row's interval of visible slots, where positions are slots or are not asked for: [lo, hi).
+__device__ __forceinline__ void row_interval(const PagedAttnParams& p, const SeqView& s, const RowView& v, bool with_pos,
+                                             int& lo, int& hi) {
+  lo = with_pos ? 0 : max(v.first, 0);
+  hi = max(v.hi, 0);
+  if (v.hi >= 0 && p.causal && p.prefix && !with_pos) hi = max(hi, min(s.len, s.prefix));
+}
+
+// The B fragments of ROWS query rows (row 8 * half + r for lane 4r + c; the thread's channels are c * D / 4 on).
+// Rows past the call's are zero and not read. bf16 rows are multiplied by a power of two that puts their largest
+// magnitude in [2^7, 2^8); `back` undoes it, for the rows 8 * half + 2c + e of the thread's scores.
 template <int D, int ROWS>
 __device__ __forceinline__ void load_q(const PagedAttnParams& p, const SeqView& s, int b, int h, int row0, int lane,
-                                       uint32_t (&qa)[D / 16][ROWS / 4], float (&back)[ROWS / 8]) {
+                                       uint32_t (&qb)[D / 16][ROWS / 4], float (&back)[ROWS / 8][2]) {
   constexpr int KS = D / 16;
   const int c = lane & 3;
 #pragma unroll
@@ -119,20 +138,14 @@ __device__ __forceinline__ void load_q(const PagedAttnParams& p, const SeqView& 
     const int i = row / p.G, hq = h * p.G + row % p.G;
     uint2 raw[KS];
     const bool live = i < s.q_len;
-    const uint16_t* q = p.q + b * p.q_sb + hq * p.q_sh + i * p.q_st;
+    const uint16_t* q = p.q + b * p.q_sb + hq * p.q_sh + i * p.q_st + c * (D / 4);
 #pragma unroll
-    for (int j = 0; j < KS / 4; ++j) {
-      uint4 v0 = make_uint4(0, 0, 0, 0), v1 = v0;
-      if (live) {
-        v0 = __ldg(reinterpret_cast<const uint4*>(q + j * 64 + c * 16));
-        v1 = __ldg(reinterpret_cast<const uint4*>(q + j * 64 + c * 16 + 8));
-      }
-      raw[4 * j] = make_uint2(v0.x, v0.y);
-      raw[4 * j + 1] = make_uint2(v0.z, v0.w);
-      raw[4 * j + 2] = make_uint2(v1.x, v1.y);
-      raw[4 * j + 3] = make_uint2(v1.z, v1.w);
+    for (int j = 0; j < KS / 2; ++j) {
+      const uint4 v = live ? __ldg(reinterpret_cast<const uint4*>(q + j * 8)) : make_uint4(0, 0, 0, 0);
+      raw[2 * j] = make_uint2(v.x, v.y);
+      raw[2 * j + 1] = make_uint2(v.z, v.w);
     }
-    back[half] = 1.0f;
+    float mine = 1.0f;
     if (p.q_bf16) {
       uint32_t top = 0;  // largest magnitude's bf16 bits
 #pragma unroll
@@ -145,7 +158,7 @@ __device__ __forceinline__ void load_q(const PagedAttnParams& p, const SeqView& 
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
       const int e = max(min(static_cast<int>(top >> 7) - 127, 119), -119);  // a row of zeros, of tiny values, of infinity
       const float f = __uint_as_float(static_cast<uint32_t>(127 + 7 - e) << 23);
-      back[half] = __uint_as_float(static_cast<uint32_t>(127 - 7 + e) << 23);
+      mine = __uint_as_float(static_cast<uint32_t>(127 - 7 + e) << 23);
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
         raw[k].x = tc::cvt_half2(__uint_as_float(raw[k].x << 16) * f, __uint_as_float(raw[k].x & 0xffff0000u) * f);
@@ -153,80 +166,164 @@ __device__ __forceinline__ void load_q(const PagedAttnParams& p, const SeqView& 
       }
     }
 #pragma unroll
+    for (int e = 0; e < 2; ++e) back[half][e] = __shfl_sync(0xffffffffu, mine, 8 * c + 4 * e);
+#pragma unroll
     for (int k = 0; k < KS; ++k) {
-      // a0: rows r, channels 0,1 of the thread's four; a1: rows r + 8; a2, a3: channels 2,3
-      qa[k][half] = raw[k].x;
-      qa[k][ROWS / 8 + half] = raw[k].y;
+      qb[k][2 * half] = raw[k].x;      // channels 0, 1 of the thread's four
+      qb[k][2 * half + 1] = raw[k].y;  // 2, 3
     }
   }
 }
 
-template <int ROWS>
-__device__ __forceinline__ void mma_rows(float (&d)[4], const uint32_t (&qa)[ROWS / 4], uint32_t b0, uint32_t b1) {
-  if (ROWS == 16) {
-    const uint32_t a[4] = {qa[0], qa[1], qa[2 % (ROWS / 4)], qa[3 % (ROWS / 4)]};
-    mma_16816(d, a, b0, b1);
-  } else {
-    const uint32_t a[4] = {qa[0], 0u, qa[1], 0u};
-    mma_16816(d, a, b0, b1);
+// ---- units: the codes of 32 tokens of a page in shared memory
+// Rows of D bytes, their 16-byte chunks permuted so that both the fragment loads of K (two rows of a thread group's
+// chunks at a time) and the transposing loads of V (one chunk of eight rows) touch all banks once.
+template <int D>
+__device__ __forceinline__ uint32_t unit_at(int row, int chunk) {
+  return row * D + ((D == 128 ? chunk ^ (row & 7) : chunk ^ ((row >> 1) & 3)) << 4);
+}
+template <int D>
+struct UnitCfg {
+  static constexpr int CODES = 32 * D;         // bytes of one tensor's codes
+  static constexpr int SCALES = CODES;         // behind K's: K and V scale
+  static constexpr int POS = SCALES + 16;      // 32 positions
+  static constexpr int K = CODES + 256;
+  static constexpr int V = CODES;
+};
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// 16 bytes, or zeros (nothing is read)
+__device__ __forceinline__ void copy16_or_zero(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// The warp copies half `half` of page slot ph (page * H + h) to `dst`: the codes of one tensor; K's with the scales of
+// both, and positions if asked for.
+template <int D, int TENSOR>
+__device__ __forceinline__ void copy_unit(const PagedPool& c, int64_t ph, int half, uint32_t dst, int lane, bool pos) {
+  constexpr int CPR = D / 16, RPI = 32 / CPR;
+  const unsigned char* from = c.code[TENSOR] + (ph * kPage + half * 32) * D + lane * 16;
+#pragma unroll
+  for (int i = 0; i < 32 / RPI; ++i) copy16(dst + unit_at<D>(i * RPI + lane / CPR, lane % CPR), from + i * 512);
+  if (TENSOR == 0) {
+    if (lane < 2) copy4(dst + UnitCfg<D>::SCALES + lane * 4, (lane ? c.scale[1] : c.scale[0]) + ph);
+    if (pos && lane < 8) copy16(dst + UnitCfg<D>::POS + lane * 16, c.pos + ph * kPage + half * 32 + lane * 4);
   }
 }
 
-// K codes of 32 keys of a page, for lane 4r + c: key 8 * nt + r, 16 channels at 64 * j + 16 * c.
-template <int D>
-__device__ __forceinline__ void load_k(const unsigned char* k, int lane, uint4 (&kr)[4][D / 64]) {
-#pragma unroll
-  for (int nt = 0; nt < 4; ++nt)
-#pragma unroll
-    for (int j = 0; j < D / 64; ++j)
-      kr[nt][j] = __ldg(reinterpret_cast<const uint4*>(k + (nt * 8 + (lane >> 2)) * D + j * 64 + (lane & 3) * 16));
-}
-
-// Raw scores of ROWS rows and 32 keys.
+// Raw scores, transposed: s[mt][half][2 * g + e] of lane 4r + c is key 16 * mt + 8 * g + r, row 8 * half + 2c + e.
+// (Keys as the products' 16 rows and queries as their 8 columns: no product has rows of nothing, and the fragments of K
+// come from the conversions in the registers that the instruction wants.)
 template <int D, int CODE, int ROWS>
-__device__ __forceinline__ void scores_32(const uint4 (&kr)[4][D / 64], const uint32_t (&qa)[D / 16][ROWS / 4],
-                                          float (&s)[4][4]) {
+__device__ __forceinline__ void scores_32(uint32_t unit, const uint32_t (&qb)[D / 16][ROWS / 4], int lane,
+                                          float (&s)[2][ROWS / 8][4]) {
 #pragma unroll
-  for (int nt = 0; nt < 4; ++nt) {
+  for (int mt = 0; mt < 2; ++mt) {
+    uint4 k[2][D / 64];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) s[nt][e] = 0.0f;
+    for (int g = 0; g < 2; ++g)
+#pragma unroll
+      for (int j = 0; j < D / 64; ++j) {
+        const uint32_t at = unit + unit_at<D>(mt * 16 + g * 8 + (lane >> 2), (lane & 3) * (D / 64) + j);
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(k[g][j].x), "=r"(k[g][j].y), "=r"(k[g][j].z), "=r"(k[g][j].w) : "r"(at));
+      }
 #pragma unroll
     for (int ks = 0; ks < D / 16; ++ks) {
-      uint32_t b0, b1;
-      codes_f16<CODE>((&kr[nt][ks >> 2].x)[ks & 3], b0, b1);
-      mma_rows<ROWS>(s[nt], qa[ks], b0, b1);
+      uint32_t a[4];
+      codes_f16<CODE>((&k[0][ks >> 2].x)[ks & 3], a[0], a[2]);
+      codes_f16<CODE>((&k[1][ks >> 2].x)[ks & 3], a[1], a[3]);
+#pragma unroll
+      for (int half = 0; half < ROWS / 8; ++half) {
+        if (ks == 0)
+          mma_16816_from_zero(s[mt][half], a, qb[ks][2 * half], qb[ks][2 * half + 1]);
+        else
+          mma_16816(s[mt][half], a, qb[ks][2 * half], qb[ks][2 * half + 1]);
+      }
     }
   }
 }
 
-// Scores to log2 units with cap, bias and masks; -inf where the row does not see the key.
-// s[nt][2 * half + e]: row half, key slot0 + 8 * nt + 2 * c + e.
-template <int ROWS, bool BIAS>
-__device__ __forceinline__ void finish_scores(const PagedAttnParams& p, const SeqView& sv, const RowView (&rv)[ROWS / 8],
-                                              const float (&f)[ROWS / 8], float cap_f, int slot0, int lane, bool masked,
-                                              const int32_t* pos, float (&s)[4][4]) {
-#pragma unroll
-  for (int nt = 0; nt < 4; ++nt)
+// What the thread's rows 8 * half + 2c + e see.
+template <int ROWS>
+struct FewRowsView {
+  RowView v[ROWS / 8][2];
+  int lo[ROWS / 8][2], hi[ROWS / 8][2];
+  int hi_max, hi_min, lo_min, lo_max;  // over the tile: bounds of the walk, and of the slots that every row sees
+
+  __device__ __forceinline__ void load(const PagedAttnParams& p, const SeqView& sv, int b, int h, int row0, int lane, bool with_pos) {
+    hi_max = 0, hi_min = INT32_MAX, lo_min = INT32_MAX, lo_max = 0;
 #pragma unroll
     for (int half = 0; half < ROWS / 8; ++half)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        float z = s[nt][2 * half + e];
-        const int key = nt * 8 + 2 * (lane & 3) + e;
-        const int slot = slot0 + key;
-        if (BIAS) {
-          z *= f[half];  // natural units
-          z = p.cap > 0.0f ? capped(z, p.cap, cap_f) : z * kLog2e;
-          const int kp = pos ? __ldg(pos + key) : slot;
-          z = fmaf(-rv[half].slope, fabsf(static_cast<float>(rv[half].pos - kp)), z);
-          const bool see = slot < sv.len && (slot < rv[half].hi || (kp < sv.prefix && rv[half].hi >= 0)) && kp >= rv[half].first;
-          z = see ? z : -INFINITY;
-        } else {
-          z *= f[half];  // log2 units
-          if (masked && slot >= rv[half].hi) z = -INFINITY;
+        const RowView r = row_view(p, sv, b, h, row0 + half * 8 + 2 * (lane & 3) + e);
+        int l, u;
+        row_interval(p, sv, r, with_pos, l, u);
+        hi_max = max(hi_max, u);
+        hi_min = min(hi_min, u);
+        lo_max = max(lo_max, l);
+        if (r.hi >= 0) {
+          lo_min = min(lo_min, l);
+          if (with_pos && p.causal && p.prefix) hi_max = sv.len;
         }
-        s[nt][2 * half + e] = z;
+        // with positions every score is masked for itself; the slots here only bound the walk
+        v[half][e] = r;
+        lo[half][e] = l;
+        hi[half][e] = with_pos ? INT32_MAX : u;
       }
+    hi_max = __reduce_max_sync(0xffffffffu, hi_max);
+    hi_min = with_pos ? INT32_MAX : __reduce_min_sync(0xffffffffu, hi_min);
+    lo_min = __reduce_min_sync(0xffffffffu, lo_min);
+    lo_max = with_pos ? 0 : __reduce_max_sync(0xffffffffu, lo_max);
+  }
+};
+
+// Scores to log2 units with cap, bias and masks; -inf where the row does not see the key. pos: the unit's positions, or NULL.
+template <int ROWS, int MODE>
+__device__ __forceinline__ void finish_scores(const PagedAttnParams& p, const SeqView& sv, const FewRowsView<ROWS>& rows,
+                                              float f, const float (&back)[ROWS / 8][2], float cap_f, int slot0, int lane,
+                                              const int32_t* pos, float (&s)[2][ROWS / 8][4]) {
+  const int prefix = p.causal && p.prefix ? sv.prefix : INT32_MIN;
+  const bool masked = slot0 + 32 > rows.hi_min || slot0 < rows.lo_max;  // (warp-uniform)
+#pragma unroll
+  for (int half = 0; half < ROWS / 8; ++half)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float fr = f * back[half][e];
+      const RowView& rv = rows.v[half][e];
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          float z = s[mt][half][2 * g + e] * fr;
+          const int key = mt * 16 + g * 8 + (lane >> 2);
+          const int slot = slot0 + key;
+          if (MODE != kPlain) {
+            z = MODE == kCap || p.cap > 0.0f ? capped(z, p.cap, cap_f) : z * kLog2e;
+            if (MODE == kGeneral) {
+              const int kp = pos ? pos[key] : slot;
+              z = fmaf(-rv.slope, fabsf(static_cast<float>(rv.pos - kp)), z);
+              if (pos) {
+                const bool see = slot < sv.len && (slot < rv.hi || (kp < prefix && rv.hi >= 0)) && kp >= rv.first;
+                z = see ? z : -INFINITY;
+              }
+            }
+          }
+          if (masked && (slot < rows.lo[half][e] || slot >= rows.hi[half][e])) z = -INFINITY;
+          s[mt][half][2 * g + e] = z;
+        }
+    }
 }
 
 // Four channels of one row to the output, and its log-sum-exp. Weights were taken as
@@ -248,20 +345,28 @@ __device__ __forceinline__ void write_row(const PagedAttnParams& p, int b, int h
 
 constexpr int kFewWarps = 4;
 
+template <int D, int ROWS>
+struct FewCfg {
+  static constexpr int RING = kFewWarps * (UnitCfg<D>::K + UnitCfg<D>::V);
+  static constexpr int JOIN = kFewWarps * ROWS * (D + 2) * 4;  // afterwards, over the units
+  static constexpr int SMEM = RING > JOIN ? RING : JOIN;
+};
+
 // Few rows: one CTA of four warps per (split of the pages, 16- or 8-row tile, key head,
-// sequence). Every warp walks 32-key units on its own with codes loaded straight into the
-// MMA fragments: channels are paired off between Q and K, and keys between the weights and
-// V, so that a thread's fragment is what one wide load brings it, and no shared memory is
-// used until the warps' results are joined. K of the next unit is loaded while this one's
-// weights are computed, V of it while the next scores are. Bound by memory: the units'
-// codes, once.
-template <int D, int CODE, int ROWS, bool BIAS>
+// sequence). Every warp walks 32-token units of codes on its own. Its own asynchronous
+// copies bring the next unit's K as soon as this one's scores are taken, and the next V as
+// soon as this one's products are: one buffer each, so that 16 warps fit an SM. (Between
+// the fragment loads, conversions and products a warp waits on itself; what carries this
+// kernel is warps. One unit more in flight with 8 warps was slower: 126 against ... us.)
+// K codes are read as the fragments of Q K^T, channels paired off between Q and K as one
+// wide load brings them; V codes by transposing 16-bit loads, which bring a thread two
+// channels of two tokens, the fragments of V^T P^T.
+template <int D, int CODE, int ROWS, int MODE>
 __global__ void __launch_bounds__(kFewWarps * 32) paged_few_kernel(const __grid_constant__ PagedAttnParams p) {
   constexpr int KS = D / 16;
   constexpr int MT = D / 16;  // 16-channel tiles of the output
   constexpr int NH = ROWS / 8;
-  __shared__ float sm_o[kFewWarps][ROWS][D];
-  __shared__ float sm_ref[kFewWarps][ROWS], sm_sum[kFewWarps][ROWS];
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int c = lane & 3, r = lane >> 2;
   // row tiles of one (sequence, head, split) are neighbours: they share its codes in L2
@@ -270,206 +375,176 @@ __global__ void __launch_bounds__(kFewWarps * 32) paged_few_kernel(const __grid_
   const int bh = blockIdx.x / (p.row_tiles * p.splits);
   const int b = bh / p.c.H, h = bh - b * p.c.H;
   const int row0 = tile * ROWS;
+  const bool with_pos = MODE == kGeneral && p.c.pos;
 
   const SeqView sv = seq_view(p, b);
-  RowView rv[NH];
-  int hi_max = -1, hi_min = INT32_MAX, first_min = INT32_MAX;
-#pragma unroll
-  for (int half = 0; half < NH; ++half) {
-    rv[half] = row_view(p, sv, b, h, row0 + half * 8 + r);
-    hi_max = max(hi_max, rv[half].hi);
-    hi_min = min(hi_min, rv[half].hi);
-    first_min = min(first_min, rv[half].first);
-  }
-  hi_max = __reduce_max_sync(0xffffffffu, hi_max);
-  hi_min = __reduce_min_sync(0xffffffffu, hi_min);
-  first_min = __reduce_min_sync(0xffffffffu, first_min);
-  // pages that any row can see
-  if (BIAS && hi_max >= 0 && p.prefix) hi_max = max(hi_max, p.c.pos ? sv.len : min(sv.len, sv.prefix));
-  int pg_lo = 0;
-  if (BIAS && p.first && !p.c.pos) pg_lo = max(0, min(first_min, hi_max)) / kPage;
-  const int pg_hi = (max(hi_max, 0) + kPage - 1) / kPage;
-  const int per = (max(0, pg_hi - pg_lo) + p.splits - 1) / p.splits;
+  FewRowsView<ROWS> view;
+  view.load(p, sv, b, h, row0, lane, with_pos);
+  const int pg_lo = min(view.lo_min, view.hi_max) / kPage, pg_hi = (view.hi_max + kPage - 1) / kPage;
+  const int per = (pg_hi - pg_lo + p.splits - 1) / p.splits;
   const int pg0 = pg_lo + split * per, pg1 = min(pg_hi, pg0 + per);
   const int units = max(0, pg1 - pg0) * 2;
 
-  uint32_t qa[KS][ROWS / 4];
-  float back[NH];
-  load_q<D, ROWS>(p, sv, b, h, row0, lane, qa, back);
-  const float qk = p.sigma * code_unit<CODE>() * (BIAS ? 1.0f : kLog2e);
-  const float cap_f = BIAS && p.cap > 0.0f ? 2.0f * kLog2e / p.cap : 0.0f;
+  // the warp's two buffers; page ids one unit further ahead than the copies
+  unsigned char* mine = smem_raw + warp * (UnitCfg<D>::K + UnitCfg<D>::V);
+  const uint32_t k_at = smem_addr(mine), v_at = k_at + UnitCfg<D>::K;
+  const float* head = reinterpret_cast<const float*>(mine + UnitCfg<D>::SCALES);
+  auto page_of = [&](int u) -> int64_t {  // page * H + h of a unit, -1: none
+    const int page = u < units ? paged_page(p.c, b, pg0 + u / 2) : -1;
+    return page < 0 ? -1 : static_cast<int64_t>(page) * p.c.H + h;
+  };
+  int64_t ph = page_of(warp), ph_next = page_of(warp + kFewWarps);
+  if (ph >= 0) copy_unit<D, 0>(p.c, ph, warp & 1, k_at, lane, with_pos);
+  copy_commit();
+  if (ph >= 0) copy_unit<D, 1>(p.c, ph, warp & 1, v_at, lane, false);
+  copy_commit();
 
-  // output of rows 8 * half + 2c + e (second index 2 * half + e): channels r * D / 8 + 2 * mt (o) and one above (od)
+  uint32_t qb[KS][ROWS / 4];
+  float back[NH][2];
+  load_q<D, ROWS>(p, sv, b, h, row0, lane, qb, back);
+  const float qk = p.sigma * code_unit<CODE>() * (MODE == kPlain ? kLog2e : 1.0f);
+  const float cap_f = MODE != kPlain && p.cap > 0.0f ? 2.0f * kLog2e / p.cap : 0.0f;
+
+  // output of rows 8 * half + 2c + e (second index 2 * half + e): channels 16 * mt + 2 * r (o) and one above (od)
   float o[MT][2 * NH], od[MT][2 * NH];
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
     for (int e = 0; e < 2 * NH; ++e) o[mt][e] = od[mt][e] = 0.0f;
-  float ref[NH], sum[NH];
+  // reference (the same on the eight lanes of a row) and sum (each lane its keys')
+  float ref[NH][2], sum[NH][2];
 #pragma unroll
-  for (int half = 0; half < NH; ++half) ref[half] = -INFINITY, sum[half] = 0.0f;
+  for (int half = 0; half < NH; ++half)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) ref[half][e] = -INFINITY, sum[half][e] = 0.0f;
 
-  uint4 kr[4][D / 64];
-  // V codes of 32 keys: for k-step kk, keys 16kk + {2c, 2c+1, 2c+8, 2c+9}, D / 8 channels at r * D / 8
-  uint32_t vr[2][4][D / 32];
-  float ks_next = 0.0f, vs_next = 0.0f;
-  const unsigned char* kbase = nullptr;
-  const unsigned char* vbase = nullptr;
-  const int32_t* pos_next = nullptr;
-  bool ok_next = false;
-  auto locate = [&](int u) {
-    const int page = paged_page(p.c, b, pg0 + u / 2);
-    ok_next = page >= 0;
-    const int64_t ph = static_cast<int64_t>(max(page, 0)) * p.c.H + h;  // a bad page's codes are read from page 0 and masked
-    ks_next = __ldg(p.c.scale[0] + ph);
-    vs_next = ok_next ? __ldg(p.c.scale[1] + ph) : 0.0f;
-    const int64_t at = (ph * kPage + (u & 1) * 32) * D;
-    kbase = p.c.code[0] + at;
-    vbase = p.c.code[1] + at;
-    pos_next = p.c.pos ? p.c.pos + ph * kPage + (u & 1) * 32 : nullptr;
-  };
-  auto load_v = [&]() {
-#pragma unroll
-    for (int kk = 0; kk < 2; ++kk)
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const unsigned char* v = vbase + (kk * 16 + 2 * c + (x & 1) + (x >> 1) * 8) * D + r * (D / 8);
-        if constexpr (D == 128) {
-          const uint4 w = __ldg(reinterpret_cast<const uint4*>(v));
-          vr[kk][x][0] = w.x, vr[kk][x][1] = w.y, vr[kk][x][2] = w.z, vr[kk][x][3] = w.w;
-        } else {
-          const uint2 w = __ldg(reinterpret_cast<const uint2*>(v));
-          vr[kk][x][0] = w.x, vr[kk][x][1] = w.y;
-        }
-      }
-  };
-  if (warp < units) {
-    locate(warp);
-    load_k<D>(kbase, lane, kr);
-    load_v();
-  }
   for (int u = warp; u < units; u += kFewWarps) {
-    const float ks = ks_next, vs = vs_next;
-    const bool ok = ok_next;
-    const int32_t* pos = pos_next;
-    const int slot0 = (pg0 + u / 2) * kPage + (u & 1) * 32;
-    float s[4][4];
-    scores_32<D, CODE, ROWS>(kr, qa, s);
-    const bool more = u + kFewWarps < units;
-    if (more) {
-      locate(u + kFewWarps);
-      load_k<D>(kbase, lane, kr);
+    const bool there = ph >= 0;  // (warp-uniform) tokens of a page out of range count as unseen
+    ph = ph_next;
+    ph_next = page_of(u + 2 * kFewWarps);
+    copy_wait<1>();
+    __syncwarp();  // K is there for every lane
+    float s[2][NH][4];
+    const float ks = head[0], vs = head[1] * code_unit<CODE>();
+    if (there) {
+      scores_32<D, CODE, ROWS>(k_at, qb, lane, s);
+      finish_scores<ROWS, MODE>(p, sv, view, ks * qk, back, cap_f, (pg0 + u / 2) * kPage + (u & 1) * 32, lane,
+                                with_pos ? reinterpret_cast<const int32_t*>(head + 4) : nullptr, s);
     }
-    float f[NH];
-#pragma unroll
-    for (int half = 0; half < NH; ++half) f[half] = ks * qk * back[half];
-    const bool masked = !ok || slot0 + 32 > hi_min;
-    finish_scores<ROWS, BIAS>(p, sv, rv, f, cap_f, slot0, lane, masked, pos, s);
-    if (!ok) {
-#pragma unroll
-      for (int nt = 0; nt < 4; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[nt][e] = -INFINITY;
+    __syncwarp();  // every lane has left K
+    if (ph >= 0) copy_unit<D, 0>(p.c, ph, u & 1, k_at, lane, with_pos);  // (units of a warp are all first or all second halves)
+    copy_commit();
+    if (!there) {
+      if (ph >= 0) copy_unit<D, 1>(p.c, ph, u & 1, v_at, lane, false);
+      copy_commit();
+      continue;
     }
-    // a row's reference only moves when its maximum passes it by 8 (weights up to 2^15)
-    float top[NH];
+    // a row's reference only moves when a score passes it by 8 (weights up to 2^15): mostly one vote
+    float top[NH][2];
     bool move = false;
 #pragma unroll
-    for (int half = 0; half < NH; ++half) {
-      float m = -INFINITY;
+    for (int half = 0; half < NH; ++half)
 #pragma unroll
-      for (int nt = 0; nt < 4; ++nt) m = fmaxf(m, fmaxf(s[nt][2 * half], s[nt][2 * half + 1]));
-      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-      top[half] = m;
-      move |= m > ref[half] + 8.0f;
-    }
+      for (int e = 0; e < 2; ++e) {
+        top[half][e] = fmaxf(fmaxf(s[0][half][e], s[0][half][2 + e]), fmaxf(s[1][half][e], s[1][half][2 + e]));
+        move |= top[half][e] > ref[half][e] + 8.0f;
+      }
     if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
       for (int half = 0; half < NH; ++half) {
-        const float to = top[half] > ref[half] + 8.0f ? top[half] : ref[half];
-        const float g = to == ref[half] ? 1.0f : tc::ex2(ref[half] - to);
-        ref[half] = to;
-        sum[half] *= g;
-        // the output's columns: rows 2c and 2c + 1 of this half, whose factors lanes 8c and 8c + 4 hold
-        const float g0 = __shfl_sync(0xffffffffu, g, 8 * c), g1 = __shfl_sync(0xffffffffu, g, 8 * c + 4);
+        float g[2];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          o[mt][2 * half] *= g0;
-          o[mt][2 * half + 1] *= g1;
-          od[mt][2 * half] *= g0;
-          od[mt][2 * half + 1] *= g1;
+        for (int e = 0; e < 2; ++e) {
+          float m = top[half][e];
+#pragma unroll
+          for (int x = 4; x < 32; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+          const float to = m > ref[half][e] + 8.0f ? m : ref[half][e];
+          g[e] = to == ref[half][e] ? 1.0f : tc::ex2(ref[half][e] - to);
+          ref[half][e] = to;
+          sum[half][e] *= g[e];
         }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            o[mt][2 * half + e] *= g[e];
+            od[mt][2 * half + e] *= g[e];
+          }
       }
     }
-    uint32_t pb[NH][4];  // weights of (half, n-tile): keys 8nt + 2c, + 1
+    uint32_t pb[NH][4];  // weights as B fragments: keys 8x + 2c, + 1 of row 8 * half + r
 #pragma unroll
     for (int half = 0; half < NH; ++half) {
-      const float base = (ref[half] == -INFINITY ? 0.0f : ref[half]) - 7.0f;
+      const float base0 = (ref[half][0] == -INFINITY ? 0.0f : ref[half][0]) - 7.0f;
+      const float base1 = (ref[half][1] == -INFINITY ? 0.0f : ref[half][1]) - 7.0f;
 #pragma unroll
-      for (int nt = 0; nt < 4; ++nt) {
-        const float p0 = tc::ex2(s[nt][2 * half] - base), p1 = tc::ex2(s[nt][2 * half + 1] - base);
-        sum[half] += p0 + p1;
-        pb[half][nt] = tc::cvt_half2(p0, p1);
+      for (int x = 0; x < 4; ++x) {
+        const float p0 = tc::ex2(s[x >> 1][half][2 * (x & 1)] - base0), p1 = tc::ex2(s[x >> 1][half][2 * (x & 1) + 1] - base1);
+        sum[half][0] += p0;
+        sum[half][1] += p1;
+        const uint32_t w = tc::cvt_half2(p0, p1);  // key 8x + r, rows 2c, 2c + 1
+        asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(pb[half][x]) : "r"(w));
       }
     }
-    const float vsu = vs * code_unit<CODE>();
+    copy_wait<1>();
+    __syncwarp();  // V is there for every lane
+    // eight keys by one 16-byte chunk of channels per matrix: the lane's register has channels 2r, 2r + 1 of keys 2c, 2c + 1
 #pragma unroll
-    for (int wd = 0; wd < D / 32; ++wd) {  // four channels of the thread's: output tiles 2wd, 2wd + 1
-      float acc[2][NH][4];
-#pragma unroll
-      for (int m = 0; m < 2; ++m)
-#pragma unroll
-        for (int half = 0; half < NH; ++half)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[m][half][e] = 0.0f;
+    for (int mt = 0; mt < MT; ++mt) {
+      uint32_t v[4];  // keys 0-7, 8-15, 16-23, 24-31
+      asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                   : "r"(v_at + unit_at<D>(lane, mt)));
+      float acc[NH][4];
 #pragma unroll
       for (int kk = 0; kk < 2; ++kk) {
-        // bytes of key pairs interleaved: channel by channel, (key 2c, key 2c + 1)
-        const uint32_t x01 = __byte_perm(vr[kk][0][wd], vr[kk][1][wd], 0x5140);
-        const uint32_t x23 = __byte_perm(vr[kk][0][wd], vr[kk][1][wd], 0x7362);
-        const uint32_t y01 = __byte_perm(vr[kk][2][wd], vr[kk][3][wd], 0x5140);
-        const uint32_t y23 = __byte_perm(vr[kk][2][wd], vr[kk][3][wd], 0x7362);
-        uint32_t a[2][4];
-        codes_f16<CODE>(x01, a[0][0], a[0][1]);
-        codes_f16<CODE>(y01, a[0][2], a[0][3]);
-        codes_f16<CODE>(x23, a[1][0], a[1][1]);
-        codes_f16<CODE>(y23, a[1][2], a[1][3]);
-#pragma unroll
-        for (int m = 0; m < 2; ++m)
-#pragma unroll
-          for (int half = 0; half < NH; ++half)
-            mma_16816(acc[m][half], a[m], pb[half][2 * kk], pb[half][2 * kk + 1]);
-      }
-#pragma unroll
-      for (int m = 0; m < 2; ++m)
+        uint32_t a[4];
+        codes_f16_of_two<CODE>(v[2 * kk], a[0], a[1]);
+        codes_f16_of_two<CODE>(v[2 * kk + 1], a[2], a[3]);
 #pragma unroll
         for (int half = 0; half < NH; ++half) {
-          const int mt = 2 * wd + m;
-          o[mt][2 * half] = fmaf(vsu, acc[m][half][0], o[mt][2 * half]);
-          o[mt][2 * half + 1] = fmaf(vsu, acc[m][half][1], o[mt][2 * half + 1]);
-          od[mt][2 * half] = fmaf(vsu, acc[m][half][2], od[mt][2 * half]);
-          od[mt][2 * half + 1] = fmaf(vsu, acc[m][half][3], od[mt][2 * half + 1]);
+          if (kk == 0)
+            mma_16816_from_zero(acc[half], a, pb[half][0], pb[half][1]);
+          else
+            mma_16816(acc[half], a, pb[half][2], pb[half][3]);
         }
+      }
+#pragma unroll
+      for (int half = 0; half < NH; ++half) {
+        o[mt][2 * half] = fmaf(vs, acc[half][0], o[mt][2 * half]);
+        o[mt][2 * half + 1] = fmaf(vs, acc[half][1], o[mt][2 * half + 1]);
+        od[mt][2 * half] = fmaf(vs, acc[half][2], od[mt][2 * half]);
+        od[mt][2 * half + 1] = fmaf(vs, acc[half][3], od[mt][2 * half + 1]);
+      }
     }
-    if (more) load_v();
+    __syncwarp();  // every lane has left V
+    if (ph >= 0) copy_unit<D, 1>(p.c, ph, u & 1, v_at, lane, false);
+    copy_commit();
   }
 
-  // join the warps
+  // join the warps, over the units
+  copy_wait<0>();
+  __syncthreads();
+  float* sm_o = reinterpret_cast<float*>(smem_raw);  // [warp][row][D]
+  float* sm_ref = sm_o + kFewWarps * ROWS * D;       // [warp][row]
+  float* sm_sum = sm_ref + kFewWarps * ROWS;
 #pragma unroll
   for (int half = 0; half < NH; ++half) {
-    sum[half] += __shfl_xor_sync(0xffffffffu, sum[half], 1);
-    sum[half] += __shfl_xor_sync(0xffffffffu, sum[half], 2);
-    if (c == 0) {
-      sm_ref[warp][half * 8 + r] = ref[half];
-      sm_sum[warp][half * 8 + r] = sum[half];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float l = sum[half][e];
+#pragma unroll
+      for (int x = 4; x < 32; x <<= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
+      if (r == 0) {
+        sm_ref[warp * ROWS + half * 8 + 2 * c + e] = ref[half][e];
+        sm_sum[warp * ROWS + half * 8 + 2 * c + e] = l;
+      }
     }
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
-      const int ch = r * (D / 8) + 2 * mt;
-      *reinterpret_cast<float2*>(&sm_o[warp][half * 8 + 2 * c][ch]) = make_float2(o[mt][2 * half], od[mt][2 * half]);
-      *reinterpret_cast<float2*>(&sm_o[warp][half * 8 + 2 * c + 1][ch]) =
-          make_float2(o[mt][2 * half + 1], od[mt][2 * half + 1]);
+      float* at = sm_o + (warp * ROWS + half * 8 + 2 * c) * D + mt * 16 + 2 * r;
+      *reinterpret_cast<float2*>(at) = make_float2(o[mt][2 * half], od[mt][2 * half]);
+      *reinterpret_cast<float2*>(at + D) = make_float2(o[mt][2 * half + 1], od[mt][2 * half + 1]);
     }
   }
   __syncthreads();
@@ -479,14 +554,15 @@ __global__ void __launch_bounds__(kFewWarps * 32) paged_few_kernel(const __grid_
     if (i >= sv.q_len) continue;
     float m = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kFewWarps; ++w) m = fmaxf(m, sm_ref[w][row]);
+    for (int w = 0; w < kFewWarps; ++w) m = fmaxf(m, sm_ref[w * ROWS + row]);
     float l = 0.0f;
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
     for (int w = 0; w < kFewWarps; ++w) {
-      const float g = sm_ref[w][row] == m ? 1.0f : tc::ex2(sm_ref[w][row] - m);  // (a NaN's sum goes on)
-      l += g * sm_sum[w][row];
-      const float4 a = *reinterpret_cast<const float4*>(&sm_o[w][row][ch]);
+      const float m_w = sm_ref[w * ROWS + row];
+      const float g = m_w == m ? 1.0f : tc::ex2(m_w - m);  // (a NaN's sum goes on)
+      l += g * sm_sum[w * ROWS + row];
+      const float4 a = *reinterpret_cast<const float4*>(sm_o + (w * ROWS + row) * D + ch);
       v.x = fmaf(g, a.x, v.x), v.y = fmaf(g, a.y, v.y), v.z = fmaf(g, a.z, v.z), v.w = fmaf(g, a.w, v.w);
     }
     if (p.splits > 1) {
@@ -499,135 +575,162 @@ __global__ void __launch_bounds__(kFewWarps * 32) paged_few_kernel(const __grid_
   }
 }
 
-// Joins the splits: one warp per row.
-template <int D>
-__global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__ PagedAttnParams p, int rows_pad) {
-  const int64_t w = (static_cast<int64_t>(blockIdx.x) * 128 + threadIdx.x) >> 5;
-  const int lane = threadIdx.x & 31;
+// Joins the splits: one CTA per row, whose WARPS warps take the splits in turn (a warp alone would wait for one split
+// after the other: 148 of them took 60 us) and meet in shared memory, always in the same order.
+template <int D, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32) paged_join_kernel(const __grid_constant__ PagedAttnParams p, int rows_pad) {
+  constexpr int C = D / 32;  // channels per lane
+  __shared__ float sm_ref[WARPS], sm_sum[WARPS];
+  __shared__ float sm_o[WARPS][D];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rows = p.n * p.G;
-  const int64_t bh = w / rows;
-  if (bh >= static_cast<int64_t>(p.B) * p.c.H) return;
-  const int row = static_cast<int>(w - bh * rows);
-  const int b = static_cast<int>(bh / p.c.H), h = static_cast<int>(bh % p.c.H);
+  const int bh = blockIdx.x / rows, row = blockIdx.x % rows;
+  const int b = bh / p.c.H, h = bh % p.c.H;
   const SeqView sv = seq_view(p, b);
   if (row / p.G >= sv.q_len) return;
   const int64_t stride = static_cast<int64_t>(p.B) * p.c.H * rows_pad;
-  const int64_t at = bh * rows_pad + row;
-  float m = -INFINITY;
-  for (int s = lane; s < p.splits; s += 32) m = fmaxf(m, p.part_ml[at + s * stride].x);
+  const int64_t at = static_cast<int64_t>(bh) * rows_pad + row;
+  float m = -INFINITY, l = 0.0f;
+  for (int s = warp + WARPS * lane; s < p.splits; s += WARPS * 32) m = fmaxf(m, __ldg(&p.part_ml[at + s * stride].x));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  float l = 0.0f;
-  const int ch = lane * 4;
-  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  for (int s = 0; s < p.splits; ++s) {
-    const float2 ml = p.part_ml[at + s * stride];
-    const float g = ml.x == m ? 1.0f : tc::ex2(ml.x - m);
+  float v[C];
+#pragma unroll
+  for (int i = 0; i < C; ++i) v[i] = 0.0f;
+#pragma unroll 8
+  for (int s = warp; s < p.splits; s += WARPS) {
+    const float2 ml = __ldg(&p.part_ml[at + s * stride]);
+    const float* o = p.part_o + (at + s * stride) * D + lane * C;
+    const float g = ml.x == m ? 1.0f : tc::ex2(ml.x - m);  // (a NaN's sum goes on)
     l = fmaf(g, ml.y, l);
-    if (ch < D) {
-      const float4 a = *reinterpret_cast<const float4*>(p.part_o + (at + s * stride) * D + ch);
-      v.x = fmaf(g, a.x, v.x), v.y = fmaf(g, a.y, v.y), v.z = fmaf(g, a.z, v.z), v.w = fmaf(g, a.w, v.w);
+    if constexpr (C == 4) {
+      const float4 a = __ldg(reinterpret_cast<const float4*>(o));
+      v[0] = fmaf(g, a.x, v[0]), v[1] = fmaf(g, a.y, v[1]), v[2] = fmaf(g, a.z, v[2]), v[3] = fmaf(g, a.w, v[3]);
+    } else {
+      const float2 a = __ldg(reinterpret_cast<const float2*>(o));
+      v[0] = fmaf(g, a.x, v[0]), v[1] = fmaf(g, a.y, v[1]);
     }
   }
-  if (ch < D) write_row<D>(p, b, h, row, ch, v, m, l);
+#pragma unroll
+  for (int i = 0; i < C; ++i) sm_o[warp][lane * C + i] = v[i];
+  if (lane == 0) sm_ref[warp] = m, sm_sum[warp] = l;
+  __syncthreads();
+  if (tid >= D / 4) return;
+  m = sm_ref[0];
+#pragma unroll
+  for (int w = 1; w < WARPS; ++w) m = fmaxf(m, sm_ref[w]);
+  l = 0.0f;
+  float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) {
+    const float g = sm_ref[w] == m ? 1.0f : tc::ex2(sm_ref[w] - m);
+    l = fmaf(g, sm_sum[w], l);
+    const float4 a = *reinterpret_cast<const float4*>(&sm_o[w][tid * 4]);
+    x.x = fmaf(g, a.x, x.x), x.y = fmaf(g, a.y, x.y), x.z = fmaf(g, a.z, x.z), x.w = fmaf(g, a.w, x.w);
+  }
+  write_row<D>(p, b, h, row, tid * 4, x, m, l);
 }
 
-// Sums of the attention weights: one warp per 32 cached tokens of a (sequence, head), whose
-// K codes stay in registers as MMA fragments while the query rows pass by in tiles of 16.
-// A token's sum runs over the rows in order, without atomics: results repeat to the bit.
-template <int D, int CODE, bool BIAS>
+constexpr int kSumStages = 3;  // K units in a warp's ring: one worked on, two on their way
+
+// Sums of the attention weights, few rows: every warp walks 32-token units of K as above, the query rows as fragments
+// in registers. A token's weights are summed over the rows of a tile by shuffles in a fixed order, and tile by tile by
+// one warp: results repeat to the bit. Bound by memory: the K codes, once per row tile.
+template <int D, int CODE, int ROWS, int MODE>
 __global__ void __launch_bounds__(kFewWarps * 32) paged_weights_kernel(const __grid_constant__ PagedAttnParams p) {
-  constexpr int KS = D / 16;
+  constexpr int KS = D / 16, NH = ROWS / 8;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int c = lane & 3, r = lane >> 2;
-  const int groups = (p.c.max_pages + 1) / 2;
-  const int bh = blockIdx.x / groups;
+  const int split = blockIdx.x % p.splits;
+  const int bh = blockIdx.x / p.splits;
   const int b = bh / p.c.H, h = bh - b * p.c.H;
-  const int u = (blockIdx.x % groups) * kFewWarps + warp;
-  const int slot0 = u * 32;
+  const bool with_pos = MODE == kGeneral && p.c.pos;
   const SeqView sv = seq_view(p, b);
-  if (slot0 >= sv.len) return;
-  const int page = paged_page(p.c, b, u / 2);
-  if (page < 0) return;
-  const int64_t ph = static_cast<int64_t>(page) * p.c.H + h;
-  uint4 kr[4][D / 64];
-  load_k<D>(p.c.code[0] + (ph * kPage + (u & 1) * 32) * D, lane, kr);
-  const float qk = __ldg(p.c.scale[0] + ph) * p.sigma * code_unit<CODE>() * (BIAS ? 1.0f : kLog2e);
-  const float cap_f = BIAS && p.cap > 0.0f ? 2.0f * kLog2e / p.cap : 0.0f;
-  const int32_t* pos = p.c.pos ? p.c.pos + ph * kPage + (u & 1) * 32 : nullptr;
-
-  float w[4][2];
-#pragma unroll
-  for (int nt = 0; nt < 4; ++nt) w[nt][0] = w[nt][1] = 0.0f;
+  const int pages = (sv.len + kPage - 1) / kPage;
+  const int per = (pages + p.splits - 1) / p.splits;
+  const int pg0 = split * per, pg1 = min(pages, pg0 + per);
+  const int units = max(0, pg1 - pg0) * 2;
   const int rows = sv.q_len * p.G;
+
+  unsigned char* ring_at = smem_raw + warp * (kSumStages * UnitCfg<D>::K);
+  const uint32_t ring = smem_addr(ring_at);
+  const float qk = p.sigma * code_unit<CODE>() * (MODE == kPlain ? kLog2e : 1.0f);
+  const float cap_f = MODE != kPlain && p.cap > 0.0f ? 2.0f * kLog2e / p.cap : 0.0f;
+  auto page_of = [&](int u) -> int64_t {  // page * H + h of a unit, -1: none
+    const int page = u < units ? paged_page(p.c, b, pg0 + u / 2) : -1;
+    return page < 0 ? -1 : static_cast<int64_t>(page) * p.c.H + h;
+  };
   int row0 = 0;
-  // rows before the first that the causal rule lets see this unit (a prefix may let every row see it)
-  if (p.causal && !(p.prefix && (p.c.pos || slot0 < sv.prefix)))
-    row0 = max(0, slot0 - (sv.len - sv.q_len)) * p.G / 16 * 16;
-  for (; row0 < rows; row0 += 16) {
-    RowView rv[2];
-    bool any = false, whole = true;
+  do {  // (once where the rows fit a tile)
+    int64_t ph[kSumStages];  // of this unit and those on their way
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      rv[half] = row_view(p, sv, b, h, row0 + half * 8 + r);
-      any |= rv[half].hi >= 0 && (pos || rv[half].first < slot0 + 32);
-      whole &= rv[half].hi >= slot0 + 32;
+    for (int i = 0; i < kSumStages; ++i) ph[i] = page_of(warp + i * kFewWarps);
+#pragma unroll
+    for (int i = 0; i < kSumStages - 1; ++i) {
+      if (ph[i] >= 0) copy_unit<D, 0>(p.c, ph[i], warp & 1, ring + i * UnitCfg<D>::K, lane, with_pos);
+      copy_commit();
     }
-    if (!__any_sync(0xffffffffu, any)) continue;
-    whole = __all_sync(0xffffffffu, whole);
-    uint32_t qa[KS][4];
-    float back[2], f[2], base[2];
-    load_q<D, 16>(p, sv, b, h, row0, lane, qa, back);
+    FewRowsView<ROWS> view;
+    view.load(p, sv, b, h, row0, lane, with_pos);
+    uint32_t qb[KS][ROWS / 4];
+    float back[NH][2], base[NH][2];
+    load_q<D, ROWS>(p, sv, b, h, row0, lane, qb, back);
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const int row = row0 + half * 8 + r;
-      f[half] = qk * back[half];
-      base[half] = INFINITY;  // no such row, or one that saw nothing
-      if (rv[half].hi >= 0) {
-        const float lse = __ldg(p.lse + (static_cast<int64_t>(b) * p.Hq + h * p.G + row % p.G) * p.n + row / p.G);
-        if (lse != -INFINITY) base[half] = lse * kLog2e;
-      }
-    }
-    float s[4][4];
-    scores_32<D, CODE, 16>(kr, qa, s);
-    finish_scores<16, BIAS>(p, sv, rv, f, cap_f, slot0, lane, !whole, pos, s);
-#pragma unroll
-    for (int nt = 0; nt < 4; ++nt)
+    for (int half = 0; half < NH; ++half)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const float w0 = base[0] == INFINITY ? 0.0f : tc::ex2(s[nt][e] - base[0]);
-        const float w1 = base[1] == INFINITY ? 0.0f : tc::ex2(s[nt][2 + e] - base[1]);
-        w[nt][e] += w0 + w1;
+        const int row = row0 + half * 8 + 2 * c + e;
+        base[half][e] = INFINITY;  // no such row, or one that saw nothing
+        if (view.v[half][e].hi >= 0) {
+          const float lse = __ldg(p.lse + (static_cast<int64_t>(b) * p.Hq + h * p.G + row % p.G) * p.n + row / p.G);
+          if (lse != -INFINITY) base[half][e] = lse * kLog2e;
+        }
       }
-  }
+    int stage = 0;
+    for (int u = warp; u < units; u += kFewWarps) {
+      copy_wait<kSumStages - 2>();
+      __syncwarp();  // this unit is there for every lane, and every lane has left the stage that is filled next
+      if (ph[kSumStages - 1] >= 0)
+        copy_unit<D, 0>(p.c, ph[kSumStages - 1], u & 1, ring + (stage == 0 ? kSumStages - 1 : stage - 1) * UnitCfg<D>::K, lane, with_pos);
+      copy_commit();
+      const int64_t at_page = ph[0];
 #pragma unroll
-  for (int nt = 0; nt < 4; ++nt)
+      for (int i = 0; i < kSumStages - 1; ++i) ph[i] = ph[i + 1];
+      ph[kSumStages - 1] = page_of(u + kSumStages * kFewWarps);
+      const uint32_t unit = ring + stage * UnitCfg<D>::K;
+      const float* head = reinterpret_cast<const float*>(ring_at + stage * UnitCfg<D>::K + UnitCfg<D>::SCALES);
+      if (++stage == kSumStages) stage = 0;
+      if (at_page < 0) continue;
+      const int32_t* pos = with_pos ? reinterpret_cast<const int32_t*>(head + 4) : nullptr;
+      const int slot0 = (pg0 + u / 2) * kPage + (u & 1) * 32;
+      float s[2][NH][4];
+      scores_32<D, CODE, ROWS>(unit, qb, lane, s);
+      finish_scores<ROWS, MODE>(p, sv, view, head[0] * qk, back, cap_f, slot0, lane, pos, s);
+      float mine = 0.0f;
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      float x = w[nt][e];
-      x += __shfl_xor_sync(0xffffffffu, x, 4);
-      x += __shfl_xor_sync(0xffffffffu, x, 8);
-      x += __shfl_xor_sync(0xffffffffu, x, 16);
-      const int key = nt * 8 + 2 * c + e;
-      if (r == 0 && slot0 + key < sv.len) {
-        float* at = p.c.weight + ph * kPage + (u & 1) * 32 + key;
-        *at = p.accumulate ? *at + x : x;
+      for (int x = 0; x < 4; ++x) {  // key 8x + r: over the thread's rows, then over the four threads of the key
+        float w = 0.0f;
+#pragma unroll
+        for (int half = 0; half < NH; ++half)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            w += base[half][e] == INFINITY ? 0.0f : tc::ex2(s[x >> 1][half][2 * (x & 1) + e] - base[half][e]);
+        w += __shfl_xor_sync(0xffffffffu, w, 1);
+        w += __shfl_xor_sync(0xffffffffu, w, 2);
+        if (x == c) mine = w;
+      }
+      const int key = 8 * c + r;
+      if (slot0 + key < sv.len) {
+        float* at = p.c.weight + at_page * kPage + (u & 1) * 32 + key;
+        *at = p.accumulate || row0 > 0 ? *at + mine : mine;
       }
     }
-}
-
-template <typename F>
-cudaError_t paged_attn_dispatch(int d, int code, bool bias, F f) {
-  using T = std::true_type;
-  using N = std::false_type;
-  auto by_bias = [&](auto dd, auto cc) { return bias ? f(dd, cc, T{}) : f(dd, cc, N{}); };
-  auto by_code = [&](auto dd) {
-    return code == kCodeInt8 ? by_bias(dd, std::integral_constant<int, kCodeInt8>{})
-                             : by_bias(dd, std::integral_constant<int, kCodeE4m3>{});
-  };
-  return d == 64 ? by_code(std::integral_constant<int, 64>{}) : by_code(std::integral_constant<int, 128>{});
+    copy_wait<0>();
+    __syncwarp();
+    row0 += ROWS;
+  } while (row0 < rows);
 }
 
 }  // namespace
-
 }  // namespace vq

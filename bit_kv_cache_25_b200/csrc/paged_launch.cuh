@@ -12,7 +12,7 @@ struct PagedPlan {
   int rows, row_tiles, splits;
 };
 
-constexpr int kFewRows = 32;  // at most so many rows per key head take the few-row kernel
+constexpr int kFewRows = 32;  // at most so many rows per key head take the few-row kernels
 
 inline PagedPlan paged_plan(int B, int H, int G, int n, int max_pages, int sms) {
   PagedPlan plan;
@@ -26,8 +26,8 @@ inline PagedPlan paged_plan(int B, int H, int G, int n, int max_pages, int sms) 
     want = sms / base;
     most = max_pages / 8;
   } else {
-    // about three CTAs per SM; a split has two pages for each of its four warps
-    want = (3 * static_cast<int64_t>(sms) + base - 1) / base;
+    // four CTAs per SM; a split has two pages for each of its four warps
+    want = (4 * static_cast<int64_t>(sms) + base - 1) / base;
     most = (max_pages + 7) / 8;
   }
   const int64_t s = want < most ? want : most;
@@ -42,9 +42,42 @@ inline size_t paged_plan_bytes(const PagedPlan& plan, int B, int H, int D) {
   return rows * (static_cast<size_t>(D) * 4 + 8);
 }
 
-inline bool paged_biased(const PagedAttnParams& p) {
-  return p.cap > 0.0f || p.slopes || p.first || (p.prefix && p.causal);
+namespace {
+
+// Launches Kernel with `smem` bytes of dynamic shared memory, allowed once per device.
+template <auto Kernel>
+cudaError_t launch_paged(const PagedAttnParams& p, unsigned grid, int threads, int smem, cudaStream_t stream) {
+  static bool configured[kMaxDevices] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  if (!configured[dev]) {
+    e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    configured[dev] = true;
+  }
+  Kernel<<<grid, threads, smem, stream>>>(p);
+  return cudaGetLastError();
 }
+
+// f(head_dim tag, code tag, mode tag) for the call's variant.
+template <typename F>
+cudaError_t paged_variant(const PagedAttnParams& p, int code, F f) {
+  const bool general = p.slopes || (p.c.pos && (p.first || (p.prefix && p.causal)));
+  auto by_mode = [&](auto d, auto c) {
+    if (general) return f(d, c, std::integral_constant<int, kGeneral>{});
+    if (p.cap > 0.0f) return f(d, c, std::integral_constant<int, kCap>{});
+    return f(d, c, std::integral_constant<int, kPlain>{});
+  };
+  auto by_code = [&](auto d) {
+    return code == kCodeInt8 ? by_mode(d, std::integral_constant<int, kCodeInt8>{})
+                             : by_mode(d, std::integral_constant<int, kCodeE4m3>{});
+  };
+  return p.c.D == 64 ? by_code(std::integral_constant<int, 64>{}) : by_code(std::integral_constant<int, 128>{});
+}
+
+}  // namespace
 
 inline cudaError_t launch_paged_attention(PagedAttnParams& p, const PagedPlan& plan, int code, void* workspace,
                                           cudaStream_t stream) {
@@ -54,33 +87,40 @@ inline cudaError_t launch_paged_attention(PagedAttnParams& p, const PagedPlan& p
   p.part_o = static_cast<float*>(workspace);
   p.part_ml = reinterpret_cast<float2*>(p.part_o + rows * p.c.D);
   const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(p.B) * p.c.H * plan.row_tiles * plan.splits);
-  cudaError_t e = plan.rows == 256 ? launch_paged_many(p, code, grid, stream) :
-                                   paged_attn_dispatch(p.c.D, code, paged_biased(p), [&](auto d, auto c, auto bias) {
+  cudaError_t e = paged_variant(p, code, [&](auto d, auto c, auto m) {
+    constexpr int D = decltype(d)::value, CODE = decltype(c)::value, MODE = decltype(m)::value;
     if (plan.rows == 8)
-      paged_few_kernel<d(), c(), 8, bias()><<<grid, kFewWarps * 32, 0, stream>>>(p);
-    else
-      paged_few_kernel<d(), c(), 16, bias()><<<grid, kFewWarps * 32, 0, stream>>>(p);
-    return cudaGetLastError();
+      return launch_paged<paged_few_kernel<D, CODE, 8, MODE>>(p, grid, kFewWarps * 32, FewCfg<D, 8>::SMEM, stream);
+    if (plan.rows == 16)
+      return launch_paged<paged_few_kernel<D, CODE, 16, MODE>>(p, grid, kFewWarps * 32, FewCfg<D, 16>::SMEM, stream);
+    return launch_paged<paged_many_kernel<D, CODE, MODE>>(p, grid, ManyCfg<D>::THREADS, ManyCfg<D>::SMEM_ALLOC, stream);
   });
   if (e != cudaSuccess || plan.splits <= 1) return e;
-  const int64_t warps = static_cast<int64_t>(p.B) * p.c.H * p.n * p.G;
-  const unsigned blocks = static_cast<unsigned>((warps + 3) / 4);
+  const unsigned blocks = static_cast<unsigned>(static_cast<int64_t>(p.B) * p.Hq * p.n);
+  const int pad = plan.row_tiles * plan.rows;
   if (p.c.D == 64)
-    paged_join_kernel<64><<<blocks, 128, 0, stream>>>(p, plan.row_tiles * plan.rows);
+    plan.splits > 32 ? paged_join_kernel<64, 16><<<blocks, 512, 0, stream>>>(p, pad)
+                     : paged_join_kernel<64, 4><<<blocks, 128, 0, stream>>>(p, pad);
   else
-    paged_join_kernel<128><<<blocks, 128, 0, stream>>>(p, plan.row_tiles * plan.rows);
+    plan.splits > 32 ? paged_join_kernel<128, 16><<<blocks, 512, 0, stream>>>(p, pad)
+                     : paged_join_kernel<128, 4><<<blocks, 128, 0, stream>>>(p, pad);
   return cudaGetLastError();
 }
 
-inline cudaError_t launch_paged_weights(PagedAttnParams& p, int code, cudaStream_t stream) {
-  const int64_t grid = static_cast<int64_t>(p.B) * p.c.H * ((p.c.max_pages + 1) / 2);
-  if (static_cast<int64_t>(p.n) * p.G > kFewRows)
-    return many_dispatch(p, code, [&](auto d, auto c, auto m) {
-      return launch_sums_variant<d(), c(), m()>(p, static_cast<unsigned>(grid), stream);
-    });
-  return paged_attn_dispatch(p.c.D, code, paged_biased(p), [&](auto d, auto c, auto bias) {
-    paged_weights_kernel<d(), c(), bias()><<<static_cast<unsigned>(grid), kFewWarps * 32, 0, stream>>>(p);
-    return cudaGetLastError();
+inline cudaError_t launch_paged_weights(PagedAttnParams& p, int code, int sms, cudaStream_t stream) {
+  const int64_t rows = static_cast<int64_t>(p.n) * p.G;
+  return paged_variant(p, code, [&](auto d, auto c, auto m) {
+    constexpr int D = decltype(d)::value, CODE = decltype(c)::value, MODE = decltype(m)::value;
+    if (rows > kFewRows) {
+      const int64_t grid = static_cast<int64_t>(p.B) * p.c.H * ((p.c.max_pages + 1) / 2);
+      return launch_paged<paged_sums_kernel<D, CODE, MODE>>(p, static_cast<unsigned>(grid), SumCfg<D>::THREADS,
+                                                            SumCfg<D>::SMEM_ALLOC, stream);
+    }
+    p.splits = paged_plan(p.B, p.c.H, 1, 1, p.c.max_pages, sms).splits;
+    const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(p.B) * p.c.H * p.splits);
+    if (rows <= 8)
+      return launch_paged<paged_weights_kernel<D, CODE, 8, MODE>>(p, grid, kFewWarps * 32, kFewWarps * kSumStages * UnitCfg<D>::K, stream);
+    return launch_paged<paged_weights_kernel<D, CODE, 16, MODE>>(p, grid, kFewWarps * 32, kFewWarps * kSumStages * UnitCfg<D>::K, stream);
   });
 }
 

@@ -31,10 +31,6 @@
 namespace vq {
 namespace {
 
-// What the softmax has to do beyond the product: nothing but an interval of slots per
-// row; a cap too; or position-dependent terms.
-enum ManyMode : int { kManyPlain = 0, kManyCap = 1, kManyGeneral = 2 };
-
 template <int D>
 struct ManyCfg {
   static constexpr int KT = 128;
@@ -194,12 +190,12 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1) paged_many_kernel(cons
     rv.hi = max(r.hi, 0);
     int reach = rv.hi;
     if (rv.live && p.causal && p.prefix) {
-      if (MODE == kManyGeneral && p.c.pos)
+      if (MODE == kGeneral && p.c.pos)
         reach = sv.len;
       else
         reach = rv.hi = max(rv.hi, min(sv.len, sv.prefix));
     }
-    if (!(MODE == kManyGeneral && p.c.pos) && rv.live) rv.lo = max(rv.first, 0);
+    if (!(MODE == kGeneral && p.c.pos) && rv.live) rv.lo = max(rv.first, 0);
     int lo = rv.live ? rv.lo : INT32_MAX;
     int hi = rv.live ? reach : 0;
     if (lo >= hi) lo = INT32_MAX, hi = 0;
@@ -268,8 +264,8 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1) paged_many_kernel(cons
         fence_proxy_async_smem();
         warp_arrive(q_full, lane);
       }
-      const float fz = p.sigma * back * (MODE == kManyPlain ? kLog2e : 1.0f);
-      const float cap_f = MODE != kManyPlain && p.cap > 0.0f ? 2.0f * kLog2e / p.cap : 0.0f;
+      const float fz = p.sigma * back * (MODE == kPlain ? kLog2e : 1.0f);
+      const float cap_f = MODE != kPlain && p.cap > 0.0f ? 2.0f * kLog2e / p.cap : 0.0f;
       for (int j = 0; j < T; ++j) {
         const int slot0 = (t0 + j) * C::KT;
         ok = mbar_wait_warp(&h_full[j & 3], (j >> 2) & 1) && mbar_wait_warp(&s_full[qt], j & 1);
@@ -277,7 +273,7 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1) paged_many_kernel(cons
         tc::fence_after_sync();
         const float* hdr = reinterpret_cast<const float*>(sm + C::HDR0 + (j & 3) * C::HDR);
         const int* kp = reinterpret_cast<const int*>(hdr + 8);
-        const bool with_pos = MODE == kManyGeneral && p.c.pos;
+        const bool with_pos = MODE == kGeneral && p.c.pos;
         const int lo = rv.lo - slot0, hi = rv.hi - slot0;
         const bool whole = __all_sync(0xffffffffu, lo <= 0 && hi >= C::KT) && !with_pos;
         // (a page of zero scale still gives -inf where masked)
@@ -292,9 +288,9 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1) paged_many_kernel(cons
         // a score in log2 units, without the mask
         auto score = [&](float a, float f, int col) {
           float z = a * f;
-          if (MODE == kManyPlain) return z;
-          z = MODE == kManyCap || p.cap > 0.0f ? capped(z, p.cap, cap_f) : z * kLog2e;
-          if (MODE == kManyGeneral) {
+          if (MODE == kPlain) return z;
+          z = MODE == kCap || p.cap > 0.0f ? capped(z, p.cap, cap_f) : z * kLog2e;
+          if (MODE == kGeneral) {
             const int k = p.c.pos ? kp[col] : slot0 + col;
             z = fmaf(-rv.slope, fabsf(static_cast<float>(rv.pos - k)), z);
           }
@@ -309,7 +305,7 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1) paged_many_kernel(cons
           const float f = half ? f1 : f0, lc = hdr[2 + half];
           float(&x)[64] = xs[half];
           tc::tmem_wait_ld();
-          if (MODE != kManyPlain) {
+          if (MODE != kPlain) {
 #pragma unroll
             for (int i = 0; i < 64; ++i) x[i] = score(x[i], f, c0 + i);
           }
@@ -323,7 +319,7 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1) paged_many_kernel(cons
 #pragma unroll
             for (int k = 0; k < 4; ++k) mx[k] = tc::max3(mx[k], x[i + 2 * k], x[i + 2 * k + 1]);
           const float m = tc::max3(tc::max3(mx[0], x[60], x[61]), tc::max3(mx[1], x[62], x[63]), fmaxf(mx[2], mx[3]));
-          const float t = MODE == kManyPlain ? fmaf(m, f, lc) : m + lc;
+          const float t = MODE == kPlain ? fmaf(m, f, lc) : m + lc;
           const bool move = t > R + 8.0f;
           if (__any_sync(0xffffffffu, move)) {
             const float g = move ? tc::ex2(R - t) : 1.0f;
@@ -364,7 +360,7 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1) paged_many_kernel(cons
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {
               const uint64_t y = tc::f2pack(x[ch + i], x[ch + i + 1]);
-              const uint64_t z = MODE == kManyPlain ? tc::fma2(y, tc::f2pack(f, f), tc::f2pack(off, off))
+              const uint64_t z = MODE == kPlain ? tc::fma2(y, tc::f2pack(f, f), tc::f2pack(off, off))
                                                     : tc::add2(y, tc::f2pack(off, off));
               const float p0 = tc::ex2(tc::f2lo(z)), p1 = tc::ex2(tc::f2hi(z));
               sum2 = tc::add2(sum2, tc::f2pack(p0, p1));
@@ -413,7 +409,7 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1) paged_many_kernel(cons
           vs[i] = ph[i] < 0 ? -1.0f : __ldg(p.c.scale[1] + ph[i]);
         }
       }
-      if (MODE == kManyGeneral && p.c.pos) pos = ph[u >> 6] < 0 ? 0 : __ldg(p.c.pos + ph[u >> 6] * kPage + (u & 63));
+      if (MODE == kGeneral && p.c.pos) pos = ph[u >> 6] < 0 ? 0 : __ldg(p.c.pos + ph[u >> 6] * kPage + (u & 63));
     };
     load(0);
     for (int j = 0; j < T; ++j) {
@@ -439,7 +435,7 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1) paged_many_kernel(cons
           hdr[4 + i] = inv;
         }
       }
-      if (MODE == kManyGeneral && p.c.pos) reinterpret_cast<int*>(hdr + 8)[u] = pos;
+      if (MODE == kGeneral && p.c.pos) reinterpret_cast<int*>(hdr + 8)[u] = pos;
       fence_proxy_async_smem();
       warp_arrive(&k_full[j & 1], lane);
       if (lane == 0) mbar_arrive(&h_full[j & 3]);
@@ -590,43 +586,6 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1) paged_many_kernel(cons
     tc::fence_after_sync();
     tc::tmem_dealloc(tm, 512);
   }
-}
-
-template <int D, int CODE, int MODE>
-cudaError_t launch_many_variant(const PagedAttnParams& p, unsigned grid, cudaStream_t stream) {
-  using C = ManyCfg<D>;
-  static bool configured[kMaxDevices] = {};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-  if (!configured[dev]) {
-    e = cudaFuncSetAttribute(paged_many_kernel<D, CODE, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_ALLOC);
-    if (e != cudaSuccess) return e;
-    configured[dev] = true;
-  }
-  paged_many_kernel<D, CODE, MODE><<<grid, C::THREADS, C::SMEM_ALLOC, stream>>>(p);
-  return cudaGetLastError();
-}
-
-// f(head_dim tag, code tag, mode tag) for the call's variant.
-template <typename F>
-cudaError_t many_dispatch(const PagedAttnParams& p, int code, F f) {
-  const bool general = p.slopes || (p.c.pos && (p.first || (p.prefix && p.causal)));
-  auto by_mode = [&](auto d, auto c) {
-    if (general) return f(d, c, std::integral_constant<int, kManyGeneral>{});
-    if (p.cap > 0.0f) return f(d, c, std::integral_constant<int, kManyCap>{});
-    return f(d, c, std::integral_constant<int, kManyPlain>{});
-  };
-  auto by_code = [&](auto d) {
-    return code == kCodeInt8 ? by_mode(d, std::integral_constant<int, kCodeInt8>{})
-                             : by_mode(d, std::integral_constant<int, kCodeE4m3>{});
-  };
-  return p.c.D == 64 ? by_code(std::integral_constant<int, 64>{}) : by_code(std::integral_constant<int, 128>{});
-}
-
-inline cudaError_t launch_paged_many(const PagedAttnParams& p, int code, unsigned grid, cudaStream_t stream) {
-  return many_dispatch(p, code, [&](auto d, auto c, auto m) { return launch_many_variant<d(), c(), m()>(p, grid, stream); });
 }
 
 }  // namespace

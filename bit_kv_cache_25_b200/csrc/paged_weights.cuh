@@ -15,7 +15,6 @@
 
 #include <cstdint>
 
-#include "attention_pipe.cuh"
 #include "paged_many.cuh"
 
 namespace vq {
@@ -88,7 +87,7 @@ __global__ void __launch_bounds__(SumCfg<D>::THREADS, 2) paged_sums_kernel(const
   int64_t ph[2];
   many_pages(p, sv, b, h, slot0 / kPage, ph);
   const int rows = sv.q_len * p.G;
-  const bool with_pos = MODE == kManyGeneral && p.c.pos;
+  const bool with_pos = MODE == kGeneral && p.c.pos;
   int rt0 = 0;
   // row tiles that end before the causal rule lets any of their rows see this tile (a prefix may let every row)
   if (p.causal && !(p.prefix && (p.c.pos || slot0 < sv.prefix)))
@@ -145,8 +144,8 @@ __global__ void __launch_bounds__(SumCfg<D>::THREADS, 2) paged_sums_kernel(const
     const int slot = slot0 + tid;
     const bool key = a >= 0 && slot < sv.len;
     const float unit = p.q_bf16 ? 1.0f : code_unit<CODE>();
-    const float f = a < 0 ? 0.0f : __ldg(p.c.scale[0] + a) * p.sigma * unit * (MODE == kManyPlain ? kLog2e : 1.0f);
-    const float cap_f = MODE != kManyPlain && p.cap > 0.0f ? 2.0f * kLog2e / p.cap : 0.0f;
+    const float f = a < 0 ? 0.0f : __ldg(p.c.scale[0] + a) * p.sigma * unit * (MODE == kPlain ? kLog2e : 1.0f);
+    const float cap_f = MODE != kPlain && p.cap > 0.0f ? 2.0f * kLog2e / p.cap : 0.0f;
     const int kp = with_pos ? (key ? __ldg(p.c.pos + a * kPage + (tid & 63)) : 0) : slot;
     const uint32_t lane_tm = tm + (static_cast<uint32_t>(warp * 32) << 16);
     const int prefix = p.causal && p.prefix ? sv.prefix : INT32_MIN;
@@ -176,9 +175,9 @@ __global__ void __launch_bounds__(SumCfg<D>::THREADS, 2) paged_sums_kernel(const
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
           float z = x[i] * f;
-          if (MODE != kManyPlain) {
-            z = MODE == kManyCap || p.cap > 0.0f ? capped(z, p.cap, cap_f) : z * kLog2e;
-            if (MODE == kManyGeneral) z = fmaf(-meta.slope[c0 + i], fabsf(static_cast<float>(meta.pos[c0 + i] - kp)), z);
+          if (MODE != kPlain) {
+            z = MODE == kCap || p.cap > 0.0f ? capped(z, p.cap, cap_f) : z * kLog2e;
+            if (MODE == kGeneral) z = fmaf(-meta.slope[c0 + i], fabsf(static_cast<float>(meta.pos[c0 + i] - kp)), z);
           }
           z -= (&ls[i >> 2].x)[i & 3];
           if (!whole) {
@@ -243,16 +242,16 @@ __global__ void __launch_bounds__(SumCfg<D>::THREADS, 2) paged_sums_kernel(const
       for (int i = 0; i < 128 / RPI; ++i) {
         const int row = i * RPI + u / CPR;
         const int64_t at = meta.at[row];
-        cp_async16(to + (row >> 3) * 1024 + (row & 7) * 128 + (((c & 7) ^ (row & 7)) << 4),
-                   p.q + (at < 0 ? 0 : at + c * 8), at < 0 ? 0 : 16);
+        copy16_or_zero(to + (row >> 3) * 1024 + (row & 7) * 128 + (((c & 7) ^ (row & 7)) << 4),
+                   p.q + (at < 0 ? 0 : at + c * 8), at >= 0);
       }
-      cp_async_commit();
+      copy_commit();
       if (j > 0) {
-        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        copy_wait<1>();
         full(j - 1);
       }
     }
-    cp_async_wait_all();
+    copy_wait<0>();
     if (ok && T > 0) full(T - 1);
   } else {
     // ======================================================================= MMA
@@ -280,23 +279,6 @@ __global__ void __launch_bounds__(SumCfg<D>::THREADS, 2) paged_sums_kernel(const
     tc::fence_after_sync();
     tc::tmem_dealloc(tm, 256);
   }
-}
-
-template <int D, int CODE, int MODE>
-cudaError_t launch_sums_variant(const PagedAttnParams& p, unsigned grid, cudaStream_t stream) {
-  using C = SumCfg<D>;
-  static bool configured[kMaxDevices] = {};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-  if (!configured[dev]) {
-    e = cudaFuncSetAttribute(paged_sums_kernel<D, CODE, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_ALLOC);
-    if (e != cudaSuccess) return e;
-    configured[dev] = true;
-  }
-  paged_sums_kernel<D, CODE, MODE><<<grid, C::THREADS, C::SMEM_ALLOC, stream>>>(p);
-  return cudaGetLastError();
 }
 
 }  // namespace
