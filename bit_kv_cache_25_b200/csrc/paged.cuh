@@ -122,6 +122,20 @@ __device__ __forceinline__ float code_value(uint32_t byte) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(static_cast<uint16_t>(byte & 0xff)));
   return __half2float(__ushort_as_half(static_cast<uint16_t>(h2 & 0xffff)));
 }
+// The values of two codes (the low half of `pair`).
+template <int CODE>
+__device__ __forceinline__ void code_values(uint32_t pair, float& lo, float& hi) {
+  if (CODE == kCodeInt8) {
+    lo = code_value<CODE>(pair & 0xff);
+    hi = code_value<CODE>((pair >> 8) & 0xff);
+  } else {
+    uint32_t h2;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(static_cast<uint16_t>(pair)));
+    const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h2));
+    lo = v.x;
+    hi = v.y;
+  }
+}
 // {lo, hi} -> two e4m3 codes, nearest, ties to even, saturating.
 __device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi) {
   uint16_t d;
@@ -140,6 +154,11 @@ struct PagedVec<kTypeBf16> {
     return __uint_as_float((i & 1) ? (w & 0xffff0000u) : (w << 16));
   }
   static __device__ __forceinline__ uint32_t pack(float lo, float hi) { return tc::cvt_bf162(lo, hi); }
+  // running maximum of the magnitudes' bits, two values at a time, and that maximum as a float's bits
+  static __device__ __forceinline__ void top(const uint4& v, uint32_t& t) {
+    t = __vmaxu2(t, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
+  }
+  static __device__ __forceinline__ uint32_t top_bits(uint32_t t) { return max(t & 0xffffu, t >> 16) << 16; }
 };
 template <>
 struct PagedVec<kTypeF16> {
@@ -149,11 +168,20 @@ struct PagedVec<kTypeF16> {
     return __half2float(__ushort_as_half(static_cast<uint16_t>((i & 1) ? (w >> 16) : (w & 0xffff))));
   }
   static __device__ __forceinline__ uint32_t pack(float lo, float hi) { return tc::cvt_half2(lo, hi); }
+  static __device__ __forceinline__ void top(const uint4& v, uint32_t& t) { PagedVec<kTypeBf16>::top(v, t); }
+  static __device__ __forceinline__ uint32_t top_bits(uint32_t t) {
+    const uint32_t m = max(t & 0xffffu, t >> 16);
+    return m > 0x7c00u ? 0x7fffffffu : __float_as_uint(__half2float(__ushort_as_half(static_cast<uint16_t>(m))));
+  }
 };
 template <>
 struct PagedVec<kTypeF32> {
   static constexpr int N = 4;
   static __device__ __forceinline__ float get(const uint4& v, int i) { return __uint_as_float((&v.x)[i]); }
+  static __device__ __forceinline__ void top(const uint4& v, uint32_t& t) {
+    t = max(max(t, max(v.x & 0x7fffffffu, v.y & 0x7fffffffu)), max(v.z & 0x7fffffffu, v.w & 0x7fffffffu));
+  }
+  static __device__ __forceinline__ uint32_t top_bits(uint32_t t) { return t; }
 };
 
 struct PagedAppendParams {
@@ -181,7 +209,7 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const __gr
   constexpr int LPR = D / V::N;                            // lanes per row
   constexpr int RPI = kAppendThreads / LPR;                // rows per CTA load
   constexpr int R = kPage / RPI;
-  __shared__ float red[kAppendThreads / 32];
+  __shared__ uint32_t red[kAppendThreads / 32];
   const int t = blockIdx.x & 1;
   const int tile = (blockIdx.x >> 1) % p.tiles;
   const int bh = (blockIdx.x >> 1) / p.tiles;
@@ -218,19 +246,38 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const __gr
     if (slot >= lo && slot < hi)
       val[i] = __ldg(reinterpret_cast<const uint4*>(x + (first + slot - start) * p.st[t] + lane_c));
   }
-  float amax = 0.0f;
+  // largest magnitude as its bits, which order as the magnitudes do; above infinity's: a NaN
+  uint32_t top = 0;
 #pragma unroll
-  for (int i = 0; i < R; ++i)
-#pragma unroll
-    for (int j = 0; j < V::N; ++j) amax = fmaxf(amax, fabsf(V::get(val[i], j)));  // a NaN is passed over
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  if ((tid & 31) == 0) red[tid >> 5] = amax;
+  for (int i = 0; i < R; ++i) V::top(val[i], top);
+  top = V::top_bits(top);
+  top = __reduce_max_sync(0xffffffffu, top);
+  if ((tid & 31) == 0) red[tid >> 5] = top;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kAppendThreads / 32; ++w) amax = fmaxf(amax, red[w]);
-  const bool cut = amax > kPagedMost;
-  if (cut) amax = kPagedMost;
+  for (int w = 0; w < kAppendThreads / 32; ++w) top = max(top, red[w]);
+  float amax = __uint_as_float(top);
+  const bool cut = !(amax <= kPagedMost);  // something to cut, or a NaN: once more, value by value
+  if (cut) {
+    amax = 0.0f;
+#pragma unroll 1
+    for (int i = 0; i < R; ++i) {
+      uint4 v = val[0];
+#pragma unroll
+      for (int k = 1; k < R; ++k)
+        if (k == i) v = val[k];
+#pragma unroll
+      for (int j = 0; j < V::N; ++j) amax = fmaxf(amax, fabsf(V::get(v, j)));  // a NaN is passed over
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    __syncthreads();
+    if ((tid & 31) == 0) red[tid >> 5] = __float_as_uint(amax);
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kAppendThreads / 32; ++w) amax = fmaxf(amax, __uint_as_float(red[w]));
+    amax = fminf(amax, kPagedMost);
+  }
 
   const float old = lo > 0 ? p.c.scale[t][ph] : 0.0f;
   float scale = old;
@@ -293,8 +340,7 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const __gr
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         xv[j] = V::get(val[i], 4 * g + j);
-        xv[j] = xv[j] == xv[j] ? xv[j] : 0.0f;
-        if (rare) xv[j] = cut ? fminf(fmaxf(xv[j], -kPagedMost), kPagedMost) : 0.0f;
+        if (rare) xv[j] = cut && xv[j] == xv[j] ? fminf(fmaxf(xv[j], -kPagedMost), kPagedMost) : 0.0f;
       }
       if (CODE == kCodeInt8) {
         // x * inv rounded by 1.5 * 2^23, then checked: x - k * scale is exact here, so a
@@ -347,12 +393,12 @@ struct PagedReadParams {
 
 namespace {
 
-// One CTA per (sequence, head, 64 tokens, tensor); eight codes per thread load,
-// one 16-byte store (two for float32). Bound by memory.
+// One CTA per (sequence, head, 64 tokens, tensor): they lie in one page or two. All loads
+// of a thread (eight codes a row) are issued before the first is used; one 16-byte store a
+// row (two for float32). Bound by memory.
 template <int T, int CODE, int D>
-__global__ void __launch_bounds__(256) paged_read_kernel(const __grid_constant__ PagedReadParams p) {
-  constexpr int LPR = D / 8;
-  constexpr int RPI = 256 / LPR;
+__global__ void __launch_bounds__(128) paged_read_kernel(const __grid_constant__ PagedReadParams p) {
+  constexpr int LPR = D / 8, RPI = 128 / LPR, R = kPage / RPI;
   const int t = blockIdx.x & 1;
   const int tile = (blockIdx.x >> 1) % p.tiles;
   const int bh = (blockIdx.x >> 1) / p.tiles;
@@ -364,28 +410,53 @@ __global__ void __launch_bounds__(256) paged_read_kernel(const __grid_constant__
     if (start < 0 || cnt < 0) return;
     cnt = p.n;
   }
-  const int c = (threadIdx.x % LPR) * 8;
+  const int rows = min(cnt - tile * kPage, kPage);
+  if (rows <= 0) return;
+  const int64_t first = static_cast<int64_t>(start) + tile * kPage;
+  const int off = static_cast<int>(first % kPage);
+  const int64_t index = first / kPage;
+  // rows below `turn` are in the first page, the others in the next; (a page index past the table is an error)
+  const int turn = kPage - off;
+  int64_t ph[2];
 #pragma unroll
-  for (int i = 0; i < kPage / RPI; ++i) {
-    const int tok = tile * kPage + i * RPI + threadIdx.x / LPR;
-    if (tok >= cnt) continue;
-    const int64_t at = static_cast<int64_t>(start) + tok;
-    const int page = at / kPage >= p.c.max_pages ? paged_page(p.c, b, -1) : paged_page(p.c, b, static_cast<int>(at / kPage));
-    if (page < 0) continue;
-    const int64_t ph = static_cast<int64_t>(page) * p.c.H + h;
-    const uint2 w = __ldg(reinterpret_cast<const uint2*>(p.c.code[t] + (ph * kPage + at % kPage) * D + c));
-    const float s = __ldg(p.c.scale[t] + ph);
+  for (int i = 0; i < 2; ++i) {
+    ph[i] = -1;
+    if (i == 0 || rows > turn) {
+      const int page = paged_page(p.c, b, index + i < p.c.max_pages ? static_cast<int>(index + i) : -1);
+      if (page >= 0) ph[i] = static_cast<int64_t>(page) * p.c.H + h;
+    }
+  }
+  const float s0 = ph[0] >= 0 ? __ldg(p.c.scale[t] + ph[0]) : 0.0f, s1 = ph[1] >= 0 ? __ldg(p.c.scale[t] + ph[1]) : 0.0f;
+  const int c = (threadIdx.x % LPR) * 8, r0 = threadIdx.x / LPR;
+  uint2 w[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const int row = i * RPI + r0;
+    const int64_t page = row < turn ? ph[0] : ph[1];
+    w[i] = make_uint2(0, 0);
+    if (row < rows && page >= 0)
+      w[i] = __ldg(reinterpret_cast<const uint2*>(p.c.code[t] + (page * kPage + ((off + row) & (kPage - 1))) * D + c));
+  }
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const int row = i * RPI + r0;
+    if (row >= rows || (row < turn ? ph[0] : ph[1]) < 0) continue;
+    const float s = row < turn ? s0 : s1;
     float v[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(code_value<CODE>(((j < 4 ? w.x : w.y) >> (8 * (j & 3))) & 0xff), s);
-    const int64_t off = b * p.sb[t] + h * p.sh[t] + tok * p.st[t] + c;
+    for (int j = 0; j < 4; ++j) {
+      code_values<CODE>(((j < 2 ? w[i].x : w[i].y) >> (16 * (j & 1))) & 0xffffu, v[2 * j], v[2 * j + 1]);
+      v[2 * j] = __fmul_rn(v[2 * j], s);
+      v[2 * j + 1] = __fmul_rn(v[2 * j + 1], s);
+    }
+    const int64_t at = b * p.sb[t] + h * p.sh[t] + static_cast<int64_t>(tile * kPage + row) * p.st[t] + c;
     if constexpr (T == kTypeF32) {
-      float4* o = reinterpret_cast<float4*>(static_cast<float*>(p.out[t]) + off);
+      float4* o = reinterpret_cast<float4*>(static_cast<float*>(p.out[t]) + at);
       o[0] = make_float4(v[0], v[1], v[2], v[3]);
       o[1] = make_float4(v[4], v[5], v[6], v[7]);
     } else {
       using V = PagedVec<T>;
-      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out[t]) + off) =
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out[t]) + at) =
           make_uint4(V::pack(v[0], v[1]), V::pack(v[2], v[3]), V::pack(v[4], v[5]), V::pack(v[6], v[7]));
     }
   }
@@ -419,7 +490,7 @@ inline cudaError_t launch_paged_append(const PagedAppendParams& p, int type, int
 inline cudaError_t launch_paged_read(const PagedReadParams& p, int type, int code, cudaStream_t stream) {
   const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(p.B) * p.c.H * p.tiles * 2);
   return paged_dispatch(type, code, p.c.D, [&](auto t, auto c, auto d) {
-    paged_read_kernel<t(), c(), d()><<<grid, 256, 0, stream>>>(p);
+    paged_read_kernel<t(), c(), d()><<<grid, 128, 0, stream>>>(p);
     return cudaGetLastError();
   });
 }

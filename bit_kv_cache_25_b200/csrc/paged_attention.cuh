@@ -344,15 +344,16 @@ __device__ __forceinline__ void write_row(const PagedAttnParams& p, int b, int h
 }
 
 constexpr int kFewWarps = 4;
+constexpr int kFewWarpsAlone = 16;  // where one CTA takes all pages of a short sequence
 
-template <int D, int ROWS>
+template <int D, int ROWS, int WARPS>
 struct FewCfg {
-  static constexpr int RING = kFewWarps * (UnitCfg<D>::K + UnitCfg<D>::V);
-  static constexpr int JOIN = kFewWarps * ROWS * (D + 2) * 4;  // afterwards, over the units
+  static constexpr int RING = WARPS * (UnitCfg<D>::K + UnitCfg<D>::V);
+  static constexpr int JOIN = WARPS * ROWS * (D + 2) * 4;  // afterwards, over the units
   static constexpr int SMEM = RING > JOIN ? RING : JOIN;
 };
 
-// Few rows: one CTA of four warps per (split of the pages, 16- or 8-row tile, key head,
+// Few rows: one CTA of 4 (or 16) warps per (split of the pages, 16- or 8-row tile, key head,
 // sequence). Every warp walks 32-token units of codes on its own. Its own asynchronous
 // copies bring the next unit's K as soon as this one's scores are taken, and the next V as
 // soon as this one's products are: one buffer each, so that 16 warps fit an SM. (Between
@@ -361,8 +362,8 @@ struct FewCfg {
 // K codes are read as the fragments of Q K^T, channels paired off between Q and K as one
 // wide load brings them; V codes by transposing 16-bit loads, which bring a thread two
 // channels of two tokens, the fragments of V^T P^T.
-template <int D, int CODE, int ROWS, int MODE>
-__global__ void __launch_bounds__(kFewWarps * 32) paged_few_kernel(const __grid_constant__ PagedAttnParams p) {
+template <int D, int CODE, int ROWS, int MODE, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32) paged_few_kernel(const __grid_constant__ PagedAttnParams p) {
   constexpr int KS = D / 16;
   constexpr int MT = D / 16;  // 16-channel tiles of the output
   constexpr int NH = ROWS / 8;
@@ -393,7 +394,7 @@ __global__ void __launch_bounds__(kFewWarps * 32) paged_few_kernel(const __grid_
     const int page = u < units ? paged_page(p.c, b, pg0 + u / 2) : -1;
     return page < 0 ? -1 : static_cast<int64_t>(page) * p.c.H + h;
   };
-  int64_t ph = page_of(warp), ph_next = page_of(warp + kFewWarps);
+  int64_t ph = page_of(warp), ph_next = page_of(warp + WARPS);
   if (ph >= 0) copy_unit<D, 0>(p.c, ph, warp & 1, k_at, lane, with_pos);
   copy_commit();
   if (ph >= 0) copy_unit<D, 1>(p.c, ph, warp & 1, v_at, lane, false);
@@ -418,10 +419,10 @@ __global__ void __launch_bounds__(kFewWarps * 32) paged_few_kernel(const __grid_
 #pragma unroll
     for (int e = 0; e < 2; ++e) ref[half][e] = -INFINITY, sum[half][e] = 0.0f;
 
-  for (int u = warp; u < units; u += kFewWarps) {
+  for (int u = warp; u < units; u += WARPS) {
     const bool there = ph >= 0;  // (warp-uniform) tokens of a page out of range count as unseen
     ph = ph_next;
-    ph_next = page_of(u + 2 * kFewWarps);
+    ph_next = page_of(u + 2 * WARPS);
     copy_wait<1>();
     __syncwarp();  // K is there for every lane
     float s[2][NH][4];
@@ -526,8 +527,8 @@ __global__ void __launch_bounds__(kFewWarps * 32) paged_few_kernel(const __grid_
   copy_wait<0>();
   __syncthreads();
   float* sm_o = reinterpret_cast<float*>(smem_raw);  // [warp][row][D]
-  float* sm_ref = sm_o + kFewWarps * ROWS * D;       // [warp][row]
-  float* sm_sum = sm_ref + kFewWarps * ROWS;
+  float* sm_ref = sm_o + WARPS * ROWS * D;       // [warp][row]
+  float* sm_sum = sm_ref + WARPS * ROWS;
 #pragma unroll
   for (int half = 0; half < NH; ++half) {
 #pragma unroll
@@ -548,17 +549,17 @@ __global__ void __launch_bounds__(kFewWarps * 32) paged_few_kernel(const __grid_
     }
   }
   __syncthreads();
-  for (int x = tid; x < ROWS * D / 4; x += kFewWarps * 32) {
+  for (int x = tid; x < ROWS * D / 4; x += WARPS * 32) {
     const int row = x / (D / 4), ch = (x % (D / 4)) * 4;
     const int i = (row0 + row) / p.G;
     if (i >= sv.q_len) continue;
     float m = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kFewWarps; ++w) m = fmaxf(m, sm_ref[w * ROWS + row]);
+    for (int w = 0; w < WARPS; ++w) m = fmaxf(m, sm_ref[w * ROWS + row]);
     float l = 0.0f;
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-    for (int w = 0; w < kFewWarps; ++w) {
+    for (int w = 0; w < WARPS; ++w) {
       const float m_w = sm_ref[w * ROWS + row];
       const float g = m_w == m ? 1.0f : tc::ex2(m_w - m);  // (a NaN's sum goes on)
       l += g * sm_sum[w * ROWS + row];

@@ -19,6 +19,7 @@
 #include <cstdint>
 
 #include "paged.cuh"
+#include "vq_internal.h"
 
 namespace vq {
 
@@ -33,6 +34,8 @@ struct PagedEvictParams {
 namespace {
 
 constexpr int kSelectThreads = 1024;
+constexpr int kSelectBins = 2048;         // digits of 11, 11 and 10 bits
+constexpr int kSelectCached = 48 * 1024;  // keys that shared memory holds; later ones are read again for each digit
 
 __device__ __forceinline__ uint32_t weight_key(float w) {
   if (w != w) return 0x007fffffu;  // as minus infinity
@@ -40,15 +43,41 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// One CTA per (sequence, head): four passes over its weights for the digits of the cut
-// (8 bits each, counted in shared memory), one to write the kept slots in order.
-__global__ void __launch_bounds__(kSelectThreads) paged_select_kernel(const __grid_constant__ PagedEvictParams p) {
-  __shared__ int hist[256];
-  __shared__ int sm_sum[2][kSelectThreads / 32];
+// Exclusive sum of one number per thread over the CTA, and the total. `sums`: one word per warp.
+__device__ __forceinline__ int block_scan(int x, int* sums, int& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int y = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int z = __shfl_up_sync(0xffffffffu, y, o);
+    if (lane >= o) y += z;
+  }
+  if (lane == 31) sums[warp] = y;
+  __syncthreads();
+  int before = 0;
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < kSelectThreads / 32; ++w) {
+    const int s = sums[w];
+    before += w < warp ? s : 0;
+    total += s;
+  }
+  __syncthreads();
+  return before + y - x;
+}
+
+// One CTA per (sequence, head). Its keys are gathered once into shared memory (a slot's page is looked up, then its
+// weight: kept there, the digits cost no global memory); three passes for the digits of the cut, one to write the kept
+// slots in order. Counts are whole numbers: their order does not matter.
+__global__ void __launch_bounds__(kSelectThreads) paged_select_kernel(const __grid_constant__ PagedEvictParams p, int cached) {
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  uint32_t* keys = reinterpret_cast<uint32_t*>(smem_raw);
+  __shared__ int hist[kSelectBins];
+  __shared__ int sums[kSelectThreads / 32];
   __shared__ uint32_t sm_prefix;
   __shared__ int sm_want;
   const int b = blockIdx.x / p.from.H, h = blockIdx.x % p.from.H;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x;
   const int len = paged_len(p.from, p.lens, b);
   int32_t* kept = p.kept + static_cast<int64_t>(blockIdx.x) * p.keep;
   const int held = min(len, p.keep);
@@ -58,86 +87,83 @@ __global__ void __launch_bounds__(kSelectThreads) paged_select_kernel(const __gr
     for (int i = tid; i < held; i += kSelectThreads) kept[i] = i;
     return;
   }
-  const int lo = p.sinks, hi = len - p.recent;  // the tokens that compete
+  const int lo = p.sinks, hi = len - p.recent;  // the slots that compete
   const int want = p.keep - p.sinks - p.recent;
-  auto key = [&](int slot) -> uint32_t {
+  auto gather = [&](int slot) -> uint32_t {
     const int page = paged_page(p.from, b, slot / kPage);
     if (page < 0) return 0x007fffffu;
-    return weight_key(p.from.weight[(static_cast<int64_t>(page) * p.from.H + h) * kPage + slot % kPage]);
+    return weight_key(__ldg(p.from.weight + (static_cast<int64_t>(page) * p.from.H + h) * kPage + slot % kPage));
   };
+  auto key = [&](int slot) -> uint32_t { return slot < cached ? keys[slot] : gather(slot); };
+  const int there = min(len, cached);
+#pragma unroll 8
+  for (int s = tid; s < there; s += kSelectThreads) keys[s] = gather(s);
   uint32_t prefix = 0;
   int need = want;
   if (want > 0) {
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      if (tid < 256) hist[tid] = 0;
+#pragma unroll 1
+    for (int digit = 0; digit < 3; ++digit) {
+      const int shift = digit == 0 ? 21 : digit == 1 ? 10 : 0;
+      const uint32_t bins = digit == 2 ? 1023u : 2047u;
+      const uint32_t mask = digit == 0 ? 0u : ~0u << (digit == 1 ? 21 : 10);
+      hist[tid] = hist[tid + kSelectThreads] = 0;
       __syncthreads();
-      const uint32_t mask = shift == 24 ? 0u : ~0u << (shift + 8);
       for (int s = lo + tid; s < hi; s += kSelectThreads) {
         const uint32_t k = key(s);
-        if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & 0xff], 1);
+        if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & bins], 1);
       }
       __syncthreads();
-      if (warp == 0) {
-        // the highest digit d with at least `need` keys at d or above it (8 digits per lane, from the top)
-        int own[8], total = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) total += own[j] = hist[255 - (lane * 8 + j)];
-        int before = total;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int y = __shfl_up_sync(0xffffffffu, before, o);
-          if (lane >= o) before += y;
-        }
-        before -= total;
-        if (before < need && before + total >= need) {
-          int left = need - before, d = 0;
-          while (own[d] < left) left -= own[d++];
-          sm_prefix = prefix | (static_cast<uint32_t>(255 - (lane * 8 + d)) << shift);
-          sm_want = left;
-        }
+      // the highest digit with at least `need` keys at it or above: two bins per thread, from the top
+      const int top = kSelectBins - 1 - 2 * tid;
+      const int c0 = hist[top], c1 = hist[top - 1];
+      int all;
+      const int before = block_scan(c0 + c1, sums, all);
+      if (before < need && before + c0 + c1 >= need) {
+        const bool second = before + c0 < need;
+        sm_prefix = prefix | (static_cast<uint32_t>(top - second) << shift);
+        sm_want = need - before - (second ? c0 : 0);
       }
       __syncthreads();
       prefix = sm_prefix;
       need = sm_want;
     }
+  } else {
+    __syncthreads();
   }
   // prefix: the cut; `need` of the keys equal to it are kept, the lowest slots
   int done = 0, ties = 0;  // kept slots and ties before this tile of slots
+#pragma unroll 1
   for (int s0 = 0; s0 < len; s0 += kSelectThreads) {
     const int s = s0 + tid;
-    bool safe = false, above = false, tie = false;
+    bool in = false, tie = false;
     if (s < len) {
-      safe = s < lo || s >= hi;
-      if (!safe && want > 0) {
+      in = s < lo || s >= hi;
+      if (!in && want > 0) {
         const uint32_t k = key(s);
-        above = k > prefix;
+        in = k > prefix;
         tie = k == prefix;
       }
     }
-    const uint32_t tie_mask = __ballot_sync(0xffffffffu, tie), in_mask = __ballot_sync(0xffffffffu, safe || above);
-    const uint32_t below = (1u << lane) - 1u;
-    if (lane == 0) {
-      sm_sum[0][warp] = __popc(in_mask);
-      sm_sum[1][warp] = __popc(tie_mask);
-    }
-    __syncthreads();
-    int in_before = done, tie_before = ties, in_all = 0, tie_all = 0;
-    for (int w = 0; w < kSelectThreads / 32; ++w) {
-      const int a = sm_sum[0][w], t = sm_sum[1][w];
-      in_before += w < warp ? a : 0;
-      tie_before += w < warp ? t : 0;
-      in_all += a;
-      tie_all += t;
-    }
-    in_before += __popc(in_mask & below);
-    tie_before += __popc(tie_mask & below);
+    // both counts in one sum: at most 1024 of each
+    int all;
+    const int before = block_scan((in ? 1 : 0) | (tie ? 1 << 16 : 0), sums, all);
+    const int tie_before = ties + (before >> 16);
     // ties before this slot that are kept take a place each
-    const int place = in_before + min(tie_before, need);
-    if ((safe || above || (tie && tie_before < need)) && place < held) kept[place] = s;
-    done += in_all;
-    ties += tie_all;
-    __syncthreads();
+    const int place = done + (before & 0xffff) + min(tie_before, need);
+    if ((in || (tie && tie_before < need)) && place < held) kept[place] = s;
+    done += all & 0xffff;
+    ties += all >> 16;
   }
+}
+
+// Two e4m3 codes times a power of two, rounded again.
+__device__ __forceinline__ uint32_t e4m3_scaled(uint32_t pair, __half2 g) {
+  uint32_t h2;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(static_cast<uint16_t>(pair)));
+  const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&h2), g);
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(*reinterpret_cast<const uint32_t*>(&v)));
+  return r;
 }
 
 // One CTA per (destination page, head, sequence): gathers its tokens' codes.
@@ -146,6 +172,7 @@ __global__ void __launch_bounds__(128) paged_move_kernel(const __grid_constant__
   constexpr int LPR = D / 16, RPI = 128 / LPR;
   __shared__ int64_t sm_src[kPage];  // (page * H + head) * 64 + slot, -1: none
   __shared__ float sm_scale[2][kPage];
+  __shared__ double sm_ratio[2][kPage];  // old scale over the page's new one
   const int per = (p.keep + kPage - 1) / kPage;
   const int tile = blockIdx.x % per, bh = blockIdx.x / per;
   const int b = bh / p.from.H, h = bh - b * p.from.H;
@@ -175,12 +202,18 @@ __global__ void __launch_bounds__(128) paged_move_kernel(const __grid_constant__
     sm_scale[1][tid] = s1;
   }
   __syncthreads();
-#pragma unroll
-  for (int t = 0; t < 2; ++t) {
+  {  // two warps per tensor
+    const int t = tid >> 6;
     float top = fmaxf(sm_scale[t][tid & 31], sm_scale[t][32 + (tid & 31)]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (tid == 0) p.to.scale[t][dst] = top;
+    if ((tid & 63) == 0) p.to.scale[t][dst] = top;
+    const float s = sm_scale[t][tid & 63];
+    sm_ratio[t][tid & 63] = s == top ? 1.0 : static_cast<double>(s) / static_cast<double>(top);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
     const int c = (tid % LPR) * 16;
     uint4 v[kPage / RPI];
 #pragma unroll
@@ -192,29 +225,30 @@ __global__ void __launch_bounds__(128) paged_move_kernel(const __grid_constant__
     for (int i = 0; i < kPage / RPI; ++i) {
       const int slot = i * RPI + tid / LPR;
       if (slot >= held) continue;
-      const float s = sm_scale[t][slot];
-      if (s != top) {
-        // the quotient of an 8-bit and two 24-bit numbers is at least 2^-33 from any half that it
-        // does not equal: in 64 bits it rounds as the real number does
-        const double f = top > 0.0f ? static_cast<double>(s) / static_cast<double>(top) : 0.0;
+      const double f = sm_ratio[t][slot];
+      if (f != 1.0) {
+        if (CODE == kCodeInt8) {
+          // the quotient of an 8-bit and two 24-bit numbers is at least 2^-33 from any half that it
+          // does not equal: in 64 bits it rounds as the real number does
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          const uint32_t o = (&v[i].x)[w];
-          uint32_t r = 0;
-          if (CODE == kCodeInt8) {
+          for (int w = 0; w < 4; ++w) {
+            const uint32_t o = (&v[i].x)[w];
+            uint32_t r = 0;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const int k = __double2int_rn(static_cast<double>(code_value<CODE>((o >> (8 * j)) & 0xff)) * f);
               r |= (static_cast<uint32_t>(k) & 0xff) << (8 * j);
             }
-          } else {
-            const float g = static_cast<float>(f);  // a power of two
-            float x[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) x[j] = code_value<CODE>((o >> (8 * j)) & 0xff) * g;
-            r = e4m3_pair(x[0], x[1]) | (e4m3_pair(x[2], x[3]) << 16);
+            (&v[i].x)[w] = r;
           }
-          (&v[i].x)[w] = r;
+        } else {
+          // a power of two (2^-24 and less leave nothing of any code): exact in fp16 wherever the result is not 0
+          const __half2 g = __half2half2(__float2half_rn(static_cast<float>(f)));
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const uint32_t o = (&v[i].x)[w];
+            (&v[i].x)[w] = e4m3_scaled(o & 0xffffu, g) | (e4m3_scaled(o >> 16, g) << 16);
+          }
         }
       }
       *reinterpret_cast<uint4*>(p.to.code[t] + (dst * kPage + slot) * D + c) = v[i];
@@ -225,9 +259,21 @@ __global__ void __launch_bounds__(128) paged_move_kernel(const __grid_constant__
 }  // namespace
 
 inline cudaError_t launch_paged_evict(const PagedEvictParams& p, int code, cudaStream_t stream) {
+  static bool configured[kMaxDevices] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  if (!configured[dev]) {
+    e = cudaFuncSetAttribute(paged_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelectCached * 4);
+    if (e != cudaSuccess) return e;
+    configured[dev] = true;
+  }
   const unsigned heads = static_cast<unsigned>(static_cast<int64_t>(p.B) * p.from.H);
-  paged_select_kernel<<<heads, kSelectThreads, 0, stream>>>(p);
-  cudaError_t e = cudaGetLastError();
+  const int64_t slots = static_cast<int64_t>(p.from.max_pages) * kPage;
+  const int cached = static_cast<int>(slots < kSelectCached ? slots : kSelectCached);
+  paged_select_kernel<<<heads, kSelectThreads, cached * 4, stream>>>(p, cached);
+  e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const unsigned grid = heads * static_cast<unsigned>((p.keep + kPage - 1) / kPage);
   if (code == kCodeInt8) {

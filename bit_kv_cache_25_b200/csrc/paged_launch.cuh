@@ -7,11 +7,13 @@
 
 namespace vq {
 
-// rows to a tile: 8 or 16 (paged_few_kernel) or 256 (paged_many_kernel).
+// rows to a tile: 8 or 16 (paged_few_kernel, of `warps` warps) or 256 (paged_many_kernel).
 struct PagedPlan {
-  int rows, row_tiles, splits;
+  int rows, row_tiles, splits, warps;
 };
 
+// Up to so many pages a CTA of 16 warps takes a sequence whole where CTAs are few: no join after it.
+constexpr int kAlonePages = 32;
 constexpr int kFewRows = 32;  // at most so many rows per key head take the few-row kernels
 
 inline PagedPlan paged_plan(int B, int H, int G, int n, int max_pages, int sms) {
@@ -32,6 +34,11 @@ inline PagedPlan paged_plan(int B, int H, int G, int n, int max_pages, int sms) 
   }
   const int64_t s = want < most ? want : most;
   plan.splits = static_cast<int>(s > 1 ? s : 1);
+  plan.warps = kFewWarps;
+  if (plan.rows == 8 && plan.splits > 1 && max_pages <= kAlonePages) {
+    plan.splits = 1;
+    plan.warps = kFewWarpsAlone;
+  }
   return plan;
 }
 
@@ -89,10 +96,13 @@ inline cudaError_t launch_paged_attention(PagedAttnParams& p, const PagedPlan& p
   const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(p.B) * p.c.H * plan.row_tiles * plan.splits);
   cudaError_t e = paged_variant(p, code, [&](auto d, auto c, auto m) {
     constexpr int D = decltype(d)::value, CODE = decltype(c)::value, MODE = decltype(m)::value;
+    constexpr int W = kFewWarps, A = kFewWarpsAlone;
+    if (plan.rows == 8 && plan.warps == A)
+      return launch_paged<paged_few_kernel<D, CODE, 8, MODE, A>>(p, grid, A * 32, FewCfg<D, 8, A>::SMEM, stream);
     if (plan.rows == 8)
-      return launch_paged<paged_few_kernel<D, CODE, 8, MODE>>(p, grid, kFewWarps * 32, FewCfg<D, 8>::SMEM, stream);
+      return launch_paged<paged_few_kernel<D, CODE, 8, MODE, W>>(p, grid, W * 32, FewCfg<D, 8, W>::SMEM, stream);
     if (plan.rows == 16)
-      return launch_paged<paged_few_kernel<D, CODE, 16, MODE>>(p, grid, kFewWarps * 32, FewCfg<D, 16>::SMEM, stream);
+      return launch_paged<paged_few_kernel<D, CODE, 16, MODE, W>>(p, grid, W * 32, FewCfg<D, 16, W>::SMEM, stream);
     return launch_paged<paged_many_kernel<D, CODE, MODE>>(p, grid, ManyCfg<D>::THREADS, ManyCfg<D>::SMEM_ALLOC, stream);
   });
   if (e != cudaSuccess || plan.splits <= 1) return e;

@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional, Sequence
 
 import torch
@@ -59,6 +60,11 @@ class vq_paged_query(ctypes.Structure):
                 ("causal", ctypes.c_int32)]
 
 
+# the same structure packed in one call, for the binding's own use (a fifth of the time that filling fields takes)
+_QUERY = struct.Struct("@4iP3q7P2fi")
+_I64x3 = ctypes.c_int64 * 3
+
+
 def _load():
     if not os.path.exists(_LIB_PATH):
         raise ImportError(f"{_LIB_PATH} is not built; run bit_kv_cache_25_b200.build.build() first")
@@ -79,8 +85,8 @@ def _load():
         "vq_paged_append": [P(vq_paged_desc), P(vq_paged_cache), I32, I32, VP, VP, I32, I64P, I64P, VP, VP, VP, VP, VP],
         "vq_paged_read": [P(vq_paged_desc), P(vq_paged_cache), I32, I32, VP, VP, VP, VP, VP, I32, I64P, I64P, VP],
         "vq_paged_attention_workspace": [P(vq_paged_desc), I32, I32, I32, P(SZ)],
-        "vq_paged_attention": [P(vq_paged_desc), P(vq_paged_cache), P(vq_paged_query), VP, I64P, VP, VP, SZ, VP],
-        "vq_paged_weights": [P(vq_paged_desc), P(vq_paged_cache), P(vq_paged_query), VP, I32, VP],
+        "vq_paged_attention": [P(vq_paged_desc), P(vq_paged_cache), VP, VP, I64P, VP, VP, SZ, VP],
+        "vq_paged_weights": [P(vq_paged_desc), P(vq_paged_cache), VP, VP, I32, VP],
         "vq_paged_evict": [P(vq_paged_desc), P(vq_paged_cache), I32, VP, VP, P(vq_paged_desc), P(vq_paged_cache), VP, VP,
                            I32, I32, I32, VP, VP],
         "vq_poll_device_error": [P(ctypes.c_uint32)],
@@ -376,9 +382,8 @@ class PagedDesc:
         self.num_pages, self.max_pages = int(num_pages), int(max_pages)
         self.c = vq_paged_desc(self.kv_heads, self.head_dim, self.code, self.num_pages, self.max_pages)
         self.ref = ctypes.byref(self.c)
-
-    def shape(self):
-        return (self.kv_heads, self.head_dim, self.code, self.num_pages, self.max_pages)
+        self.shape = (self.kv_heads, self.head_dim, self.code, self.num_pages, self.max_pages)
+        self._workspace = {}  # (device, batch, q_heads, n) -> bytes
 
 
 class PagedCache:
@@ -415,6 +420,7 @@ class PagedCache:
         self._pos = pool("pos", pos, slots, (torch.int32,), positions)
         self._weight = pool("weight", weight, slots, _F32, weights)
         self.device = self._k.device
+        self.index = self._k.get_device()  # -1: not on a GPU
         self.c = vq_paged_cache(*(None if t is None else t.data_ptr() for t in
                                   (self._k, self._v, self._k_scale, self._v_scale, self._pos, self._weight)))
         self.ref = ctypes.byref(self.c)
@@ -432,15 +438,19 @@ class PagedCache:
                    (self._k, self._v, self._k_scale, self._v_scale, self._pos, self._weight) if t is not None)
 
 
-def _paged_cache_check(desc: PagedDesc, cache: PagedCache):
-    if cache.desc is not desc and cache.desc.shape() != desc.shape():
+def _paged_cache_check(desc: PagedDesc, cache: PagedCache) -> int:
+    """Index of the cache's device."""
+    if cache._desc is not desc and cache._desc.shape != desc.shape:
         raise ValueError("the cache was made for another descriptor")
-    if cache.device.type != "cuda":
+    if cache.index < 0:
         raise ValueError(f"the cache is on {cache.device}, not a CUDA device")
-    return cache.device
+    return cache.index
 
 
-def _array(name: str, t: Optional[torch.Tensor], shape, device, dtype=torch.int32, optional=True):
+_I32 = torch.int32
+
+
+def _array(name: str, t: Optional[torch.Tensor], shape, device: int, dtype=_I32, optional=True):
     """Device address of a contiguous array argument; None if it is left out."""
     if t is None:
         if optional:
@@ -448,21 +458,21 @@ def _array(name: str, t: Optional[torch.Tensor], shape, device, dtype=torch.int3
         raise ValueError(f"{name} is missing")
     if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} is {t.dtype} of shape {tuple(t.shape)}, expected contiguous {dtype} of {tuple(shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not on {device} with the cache")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, not with the cache")
     return t.data_ptr()
 
 
-def _view(name: str, t: torch.Tensor, shape, device):
+def _view(name: str, t: torch.Tensor, shape, device: int):
     """Strides of a [B][H][n][D] argument with channels contiguous."""
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    s = t.stride()
-    if s[3] != 1:
+    b, h, n, d = t.stride()
+    if d != 1:
         raise ValueError(f"{name}: the channel dimension must be contiguous")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not on {device} with the cache")
-    return (ctypes.c_int64 * 3)(s[0], s[1], s[2])
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, not with the cache")
+    return b, h, n
 
 
 def _paged_dtype(name: str, t: torch.Tensor, allowed) -> int:
@@ -473,24 +483,28 @@ def _paged_dtype(name: str, t: torch.Tensor, allowed) -> int:
 
 
 def _rows(name: str, t: torch.Tensor, heads: Optional[int], desc: PagedDesc):
-    if t.dim() != 4:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [batch][heads][n][{desc.head_dim}]")
-    b, h, n, d = t.shape
-    if d != desc.head_dim or (heads is not None and h != heads):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [batch][{heads or 'heads'}][n][{desc.head_dim}]")
-    if b < 1 or n < 1:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}: batch and n must be at least 1")
-    return b, h, n
+    shape = t.shape
+    if len(shape) != 4 or shape[3] != desc.head_dim or (heads is not None and shape[1] != heads):
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected [batch][{heads or 'heads'}][n][{desc.head_dim}]")
+    if shape[0] < 1 or shape[2] < 1:
+        raise ValueError(f"{name} has shape {tuple(shape)}: batch and n must be at least 1")
+    return shape
 
 
-def _on(device: torch.device, stream, call):
-    """Run call(stream handle) with `device` current, on `stream` or the device's current stream."""
-    if device.index is not None and device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            return _on(device, stream, call)
+def _handle(device: int, stream):
+    """The stream a call runs on: the one given, or the device's current one."""
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    _check(call(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)))
+        return torch.cuda.current_stream(device).cuda_stream
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _on(device: int, stream, call):
+    """call(stream handle) with `device` current."""
+    if device == torch.cuda.current_device():
+        _check(call(_handle(device, stream)))
+    else:
+        with torch.cuda.device(device):
+            _check(call(_handle(device, stream)))
 
 
 def vq_paged_append(desc: PagedDesc, cache: PagedCache, block_table: torch.Tensor, start: torch.Tensor,
@@ -499,11 +513,11 @@ def vq_paged_append(desc: PagedDesc, cache: PagedCache, block_table: torch.Tenso
     """Quantize k, v [B][kv_heads][n][D] (bf16, fp16, fp32) into the sequences' pages as
     tokens start[b] .. start[b] + counts[b] - 1 (counts None: n)."""
     dev = _paged_cache_check(desc, cache)
-    B, _, n = _rows("k", k, desc.kv_heads, desc)
+    B, _, n, _ = _rows("k", k, desc.kv_heads, desc)
     if k.dtype != v.dtype:
         raise ValueError("k and v must have the same dtype")
     dt = _paged_dtype("k", k, (VQ_BF16, VQ_F16, VQ_F32))
-    ks, vs = _view("k", k, k.shape, dev), _view("v", v, k.shape, dev)
+    ks, vs = _I64x3(*_view("k", k, k.shape, dev)), _I64x3(*_view("v", v, k.shape, dev))
     table = _array("block_table", block_table, (B, desc.max_pages), dev, optional=False)
     start = _array("start", start, (B,), dev, optional=False)
     counts, pos = _array("counts", counts, (B,), dev), _array("pos", pos, (B,), dev)
@@ -515,11 +529,12 @@ def vq_paged_read(desc: PagedDesc, cache: PagedCache, block_table: torch.Tensor,
                   k_out: torch.Tensor, v_out: torch.Tensor, counts: Optional[torch.Tensor] = None, stream=None):
     """Dequantize tokens start[b] .. start[b] + counts[b] - 1 into k_out, v_out [B][kv_heads][n][D]."""
     dev = _paged_cache_check(desc, cache)
-    B, _, n = _rows("k_out", k_out, desc.kv_heads, desc)
+    B, _, n, _ = _rows("k_out", k_out, desc.kv_heads, desc)
     if k_out.dtype != v_out.dtype:
         raise ValueError("k_out and v_out must have the same dtype")
     dt = _paged_dtype("k_out", k_out, (VQ_BF16, VQ_F16, VQ_F32))
-    ks, vs = _view("k_out", k_out, k_out.shape, dev), _view("v_out", v_out, k_out.shape, dev)
+    ks = _I64x3(*_view("k_out", k_out, k_out.shape, dev))
+    vs = _I64x3(*_view("v_out", v_out, k_out.shape, dev))
     table = _array("block_table", block_table, (B, desc.max_pages), dev, optional=False)
     start = _array("start", start, (B,), dev, optional=False)
     counts = _array("counts", counts, (B,), dev)
@@ -528,15 +543,17 @@ def vq_paged_read(desc: PagedDesc, cache: PagedCache, block_table: torch.Tensor,
 
 
 def _paged_query(desc, block_table, lens, q, softmax_scale, q_lens, q_pos, prefix, first, slopes, softcap, causal, dev):
-    B, Hq, n = _rows("q", q, None, desc)
+    """(shape of q, vq_paged_query as bytes)."""
+    shape = B, Hq, n, _ = _rows("q", q, None, desc)
     dt = _paged_dtype("q", q, (VQ_BF16, VQ_F16))
-    qs = _view("q", q, q.shape, dev)
-    return vq_paged_query(B, Hq, n, dt, q.data_ptr(), qs,
-                          _array("block_table", block_table, (B, desc.max_pages), dev, optional=False),
-                          _array("lens", lens, (B,), dev, optional=False), _array("q_lens", q_lens, (B,), dev),
-                          _array("q_pos", q_pos, (B,), dev), _array("prefix", prefix, (B,), dev),
-                          _array("first", first, (B, n), dev), _array("slopes", slopes, (Hq,), dev, torch.float32),
-                          softmax_scale, softcap, int(bool(causal)))
+    sb, sh, st = _view("q", q, shape, dev)
+    per = (B,)
+    return shape, _QUERY.pack(
+        B, Hq, n, dt, q.data_ptr(), sb, sh, st, _array("block_table", block_table, (B, desc.max_pages), dev, optional=False),
+        _array("lens", lens, per, dev, optional=False), _array("q_lens", q_lens, per, dev) or 0,
+        _array("q_pos", q_pos, per, dev) or 0, _array("prefix", prefix, per, dev) or 0,
+        _array("first", first, (B, n), dev) or 0, _array("slopes", slopes, (Hq,), dev, torch.float32) or 0,
+        softmax_scale, softcap, 1 if causal else 0)
 
 
 def vq_paged_attention_workspace(desc: PagedDesc, batch: int, q_heads: int, n: int) -> int:
@@ -555,30 +572,32 @@ def vq_paged_attention(desc: PagedDesc, cache: PagedCache, block_table: torch.Te
     vq.h's. workspace: a contiguous uint8 tensor of vq_paged_attention_workspace bytes that no
     call running at the same time uses; None: allocated for this call."""
     dev = _paged_cache_check(desc, cache)
-    query = _paged_query(desc, block_table, lens, q, softmax_scale, q_lens, q_pos, prefix, first, slopes, softcap,
-                         causal, dev)
-    if out.dtype != q.dtype:
+    shape, query = _paged_query(desc, block_table, lens, q, softmax_scale, q_lens, q_pos, prefix, first, slopes, softcap,
+                                causal, dev)
+    if out.dtype is not q.dtype:
         raise ValueError(f"out is {out.dtype}, q is {q.dtype}: they must have the same dtype")
-    os_ = _view("out", out, q.shape, dev)
-    lse = _array("lse", lse, q.shape[:3], dev, torch.float32)
-    if workspace is not None:
-        if workspace.device != dev or not workspace.is_contiguous():
-            raise ValueError(f"workspace must be contiguous on {dev}")
+    os_ = _I64x3(*_view("out", out, shape, dev))
+    lse = _array("lse", lse, shape[:3], dev, torch.float32)
+    if workspace is not None and (workspace.get_device() != dev or not workspace.is_contiguous()):
+        raise ValueError("workspace must be contiguous and with the cache")
+    B, Hq, n, _ = shape
 
     def call(s):
-        size = vq_paged_attention_workspace(desc, query.batch, query.q_heads, query.n)
+        size = desc._workspace.get((dev, B, Hq, n))
+        if size is None:
+            size = desc._workspace[(dev, B, Hq, n)] = vq_paged_attention_workspace(desc, B, Hq, n)
         ws = workspace
         if ws is None and size:
             # from the pool of the stream that the call runs on: memory goes back to it in its order
             if stream is None:
-                ws = torch.empty(size, dtype=torch.uint8, device=dev)
+                ws = torch.empty(size, dtype=torch.uint8, device=cache.device)
             else:
                 on = stream if hasattr(stream, "cuda_stream") else (
-                    torch.cuda.ExternalStream(int(stream), dev) if int(stream) else torch.cuda.default_stream(dev))
+                    torch.cuda.ExternalStream(int(stream), cache.device) if int(stream) else torch.cuda.default_stream(cache.device))
                 with torch.cuda.stream(on):
-                    ws = torch.empty(size, dtype=torch.uint8, device=dev)
+                    ws = torch.empty(size, dtype=torch.uint8, device=cache.device)
         ptr, have = (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
-        return _lib.vq_paged_attention(desc.ref, cache.ref, ctypes.byref(query), out.data_ptr(), os_, lse, ptr, have, s)
+        return _lib.vq_paged_attention(desc.ref, cache.ref, query, out.data_ptr(), os_, lse, ptr, have, s)
 
     _on(dev, stream, call)
 
@@ -592,11 +611,10 @@ def vq_paged_weights(desc: PagedDesc, cache: PagedCache, block_table: torch.Tens
     dev = _paged_cache_check(desc, cache)
     if cache.weight is None:
         raise ValueError("the cache has no weight")
-    query = _paged_query(desc, block_table, lens, q, softmax_scale, q_lens, q_pos, prefix, first, slopes, softcap,
-                         causal, dev)
-    lse = _array("lse", lse, q.shape[:3], dev, torch.float32, optional=False)
-    _on(dev, stream, lambda s: _lib.vq_paged_weights(desc.ref, cache.ref, ctypes.byref(query), lse,
-                                                     int(bool(accumulate)), s))
+    shape, query = _paged_query(desc, block_table, lens, q, softmax_scale, q_lens, q_pos, prefix, first, slopes, softcap,
+                                causal, dev)
+    lse = _array("lse", lse, shape[:3], dev, torch.float32, optional=False)
+    _on(dev, stream, lambda s: _lib.vq_paged_weights(desc.ref, cache.ref, query, lse, 1 if accumulate else 0, s))
 
 
 def vq_paged_evict(desc: PagedDesc, cache: PagedCache, block_table: torch.Tensor, lens: torch.Tensor,
@@ -606,7 +624,7 @@ def vq_paged_evict(desc: PagedDesc, cache: PagedCache, block_table: torch.Tensor
     the pages of to_table; writes to_lens [B] and the source slots kept [B][kv_heads][keep]."""
     dev = _paged_cache_check(desc, cache)
     if _paged_cache_check(to_desc, to) != dev:
-        raise ValueError(f"the caches are on {dev} and {to.device}")
+        raise ValueError(f"the caches are on {cache.device} and {to.device}")
     if cache.weight is None:
         raise ValueError("the cache has no weight")
     if lens.dim() != 1 or lens.shape[0] < 1:

@@ -166,7 +166,7 @@ def test_binding_refuses_host_tensors_and_other_descriptors():
 
 def test_binding_refuses_arrays_that_do_not_fit(monkeypatch):
     desc, cache = _pool()
-    monkeypatch.setattr(vq, "_paged_cache_check", lambda d, c: torch.device("cpu"))
+    monkeypatch.setattr(vq, "_paged_cache_check", lambda d, c: -1)
     x = torch.zeros(2, 3, 4, 64, dtype=torch.bfloat16)
     ints = torch.zeros(2, dtype=torch.int32)
     table = torch.zeros(2, 4, dtype=torch.int32)
@@ -203,3 +203,14 @@ def test_launch_without_gpu_reports_cuda_error():
     if torch.cuda.is_available():
         pytest.skip("a GPU is present")
     assert _append() == vq.VQ_ERR_CUDA and _evict() == vq.VQ_ERR_CUDA and _attention() == vq.VQ_ERR_CUDA
+
+
+def test_packed_query_is_the_c_structure():
+    fields = [2, 6, 4, 2, 0x10, 1, 2, 3, 0x20, 0x30, 0x40, 0x50, 0x60, 0x70, 0x80, 0.5, 30.0, 1]
+    raw = vq._QUERY.pack(*fields)
+    q = vq.vq_paged_query.from_buffer_copy(raw.ljust(ctypes.sizeof(vq.vq_paged_query), b"\0"))
+    got = []
+    for name, _ in vq.vq_paged_query._fields_:
+        v = getattr(q, name)
+        got += list(v) if name == "q_strides" else [v]
+    assert got == fields and ctypes.sizeof(vq.vq_paged_query) - len(raw) in (0, 4)
