@@ -72,17 +72,28 @@ __device__ __forceinline__ float capped(float z, float cap, float two_log2e_over
   const float e = tc::ex2(z * two_log2e_over_cap);
   return (cap - __fdividef(2.0f * cap, e + 1.0f)) * kLog2e;
 }
+// The same of z = a * f where |z| <= cap / 4: tanh(x) = x * P(x^2), P of degree 2 interpolated at the Chebyshev nodes
+// of [0, 1/16] (4.2e-07 of itself off at most). Two multiply-adds in place of two more turns of the exponential unit, which
+// most scores are small enough for: a warp decides for all of its values.
+constexpr float kCapSmall = 0.25f;
+__device__ __forceinline__ float capped_small(float a, float f_over_cap, float cap_log2e) {
+  const float x = a * f_over_cap, y = x * x;
+  const float t = fmaf(fmaf(0.1284143328666687f * cap_log2e, y, -0.3332189619541168f * cap_log2e), y, 0.9999995827674866f * cap_log2e);
+  return x * t;
+}
 
 // What a row sees: slots [0, hi), or positions below `prefix` up to slot `len`, from position `first` on.
 struct RowView {
   int hi;      // one past the last slot that the causal rule (or the length) allows; -1: no such query
   int first;   // lowest position seen
-  int pos;     // the query's own position
+  float pos;   // the query's own position, counted from the call's first query of the sequence
   float slope; // distance bias per position, in log2 units
 };
 
+// pos0: position of the first query. Distances are taken between positions counted from it, in float32: exact below
+// 2^24, and off by 2^-24 of the distance (and of n) beyond.
 struct SeqView {
-  int len, q_len, prefix;
+  int len, q_len, prefix, pos0;
 };
 
 __device__ __forceinline__ SeqView seq_view(const PagedAttnParams& p, int b) {
@@ -94,6 +105,7 @@ __device__ __forceinline__ SeqView seq_view(const PagedAttnParams& p, int b) {
     s.q_len = s.q_len < 0 ? 0 : p.n;
   }
   s.prefix = p.prefix ? __ldg(p.prefix + b) : 0;
+  s.pos0 = p.q_pos ? __ldg(p.q_pos + b) : s.len - s.q_len;
   return s;
 }
 
@@ -102,12 +114,12 @@ __device__ __forceinline__ RowView row_view(const PagedAttnParams& p, const SeqV
   const int i = row / p.G;
   v.hi = -1;
   v.first = INT32_MAX;
-  v.pos = 0;
+  v.pos = 0.0f;
   v.slope = 0.0f;
   if (i >= s.q_len) return v;
   v.hi = p.causal ? max(0, min(s.len, s.len - s.q_len + i + 1)) : s.len;
   v.first = p.first ? __ldg(p.first + static_cast<int64_t>(b) * p.n + i) : INT32_MIN;
-  v.pos = p.q_pos ? __ldg(p.q_pos + b) + i : s.len - s.q_len + i;
+  v.pos = static_cast<float>(i);
   v.slope = p.slopes ? __ldg(p.slopes + h * p.G + row % p.G) * kLog2e : 0.0f;
   return v;
 }
@@ -117,11 +129,11 @@ __device__ __forceinline__ RowView row_view(const PagedAttnParams& p, const SeqV
 enum PagedMode : int { kPlain = 0, kCap = 1, kGeneral = 2 };
 
 // A row's interval of visible slots, where positions are slots or are not asked for: [lo, hi).
-__device__ __forceinline__ void row_interval(const PagedAttnParams& p, const SeqView& s, const RowView& v, bool with_pos,
+__device__ __forceinline__ void row_interval(const PagedAttnParams& p, const SeqView& s, const RowView& v, bool by_pos,
                                              int& lo, int& hi) {
-  lo = with_pos ? 0 : max(v.first, 0);
+  lo = by_pos ? 0 : max(v.first, 0);
   hi = max(v.hi, 0);
-  if (v.hi >= 0 && p.causal && p.prefix && !with_pos) hi = max(hi, min(s.len, s.prefix));
+  if (v.hi >= 0 && p.causal && p.prefix && !by_pos) hi = max(hi, min(s.len, s.prefix));
 }
 
 // The B fragments of ROWS query rows (row 8 * half + r for lane 4r + c; the thread's channels are c * D / 4 on).
@@ -261,7 +273,7 @@ struct FewRowsView {
   int lo[ROWS / 8][2], hi[ROWS / 8][2];
   int hi_max, hi_min, lo_min, lo_max;  // over the tile: bounds of the walk, and of the slots that every row sees
 
-  __device__ __forceinline__ void load(const PagedAttnParams& p, const SeqView& sv, int b, int h, int row0, int lane, bool with_pos) {
+  __device__ __forceinline__ void load(const PagedAttnParams& p, const SeqView& sv, int b, int h, int row0, int lane, bool by_pos) {
     hi_max = 0, hi_min = INT32_MAX, lo_min = INT32_MAX, lo_max = 0;
 #pragma unroll
     for (int half = 0; half < ROWS / 8; ++half)
@@ -269,23 +281,23 @@ struct FewRowsView {
       for (int e = 0; e < 2; ++e) {
         const RowView r = row_view(p, sv, b, h, row0 + half * 8 + 2 * (lane & 3) + e);
         int l, u;
-        row_interval(p, sv, r, with_pos, l, u);
+        row_interval(p, sv, r, by_pos, l, u);
         hi_max = max(hi_max, u);
         hi_min = min(hi_min, u);
         lo_max = max(lo_max, l);
         if (r.hi >= 0) {
           lo_min = min(lo_min, l);
-          if (with_pos && p.causal && p.prefix) hi_max = sv.len;
+          if (by_pos && p.causal && p.prefix) hi_max = sv.len;
         }
         // with positions every score is masked for itself; the slots here only bound the walk
         v[half][e] = r;
         lo[half][e] = l;
-        hi[half][e] = with_pos ? INT32_MAX : u;
+        hi[half][e] = by_pos ? INT32_MAX : u;
       }
     hi_max = __reduce_max_sync(0xffffffffu, hi_max);
-    hi_min = with_pos ? INT32_MAX : __reduce_min_sync(0xffffffffu, hi_min);
+    hi_min = by_pos ? INT32_MAX : __reduce_min_sync(0xffffffffu, hi_min);
     lo_min = __reduce_min_sync(0xffffffffu, lo_min);
-    lo_max = with_pos ? 0 : __reduce_max_sync(0xffffffffu, lo_max);
+    lo_max = by_pos ? 0 : __reduce_max_sync(0xffffffffu, lo_max);
   }
 };
 
@@ -296,34 +308,45 @@ __device__ __forceinline__ void finish_scores(const PagedAttnParams& p, const Se
                                               const int32_t* pos, float (&s)[2][ROWS / 8][4]) {
   const int prefix = p.causal && p.prefix ? sv.prefix : INT32_MIN;
   const bool masked = slot0 + 32 > rows.hi_min || slot0 < rows.lo_max;  // (warp-uniform)
+  const bool by_pos = MODE == kGeneral && pos && (p.first || (p.prefix && p.causal));
+  const bool cap = MODE == kCap || (MODE == kGeneral && p.cap > 0.0f);
+  float fr[ROWS / 8][2];
 #pragma unroll
   for (int half = 0; half < ROWS / 8; ++half)
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const float fr = f * back[half][e];
-      const RowView& rv = rows.v[half][e];
+    for (int e = 0; e < 2; ++e) fr[half][e] = f * back[half][e];
 #pragma unroll
-      for (int mt = 0; mt < 2; ++mt)
+  for (int x = 0; x < 4; ++x) {
+    const int key = 8 * x + (lane >> 2), slot = slot0 + key;
+    int kp = slot;
+    float kf = 0.0f;
+    if (MODE == kGeneral) {
+      if (pos) kp = pos[key];
+      kf = static_cast<float>(kp - sv.pos0);
+    }
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          float z = s[mt][half][2 * g + e] * fr;
-          const int key = mt * 16 + g * 8 + (lane >> 2);
-          const int slot = slot0 + key;
-          if (MODE != kPlain) {
-            z = MODE == kCap || p.cap > 0.0f ? capped(z, p.cap, cap_f) : z * kLog2e;
-            if (MODE == kGeneral) {
-              const int kp = pos ? pos[key] : slot;
-              z = fmaf(-rv.slope, fabsf(static_cast<float>(rv.pos - kp)), z);
-              if (pos) {
-                const bool see = slot < sv.len && (slot < rv.hi || (kp < prefix && rv.hi >= 0)) && kp >= rv.first;
-                z = see ? z : -INFINITY;
-              }
+    for (int half = 0; half < ROWS / 8; ++half)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const RowView& rv = rows.v[half][e];
+        float z = s[x >> 1][half][2 * (x & 1) + e];
+        if (MODE == kPlain) {
+          z *= fr[half][e];
+        } else {
+          z *= fr[half][e];
+          z = cap ? capped(z, p.cap, cap_f) : z * kLog2e;
+          if (MODE == kGeneral) {
+            z = fmaf(-rv.slope, fabsf(rv.pos - kf), z);
+            if (by_pos) {
+              const bool see = slot < sv.len && (slot < rv.hi || (kp < prefix && rv.hi >= 0)) && kp >= rv.first;
+              z = see ? z : -INFINITY;
             }
           }
-          if (masked && (slot < rows.lo[half][e] || slot >= rows.hi[half][e])) z = -INFINITY;
-          s[mt][half][2 * g + e] = z;
         }
-    }
+        if (masked && (slot < rows.lo[half][e] || slot >= rows.hi[half][e])) z = -INFINITY;
+        s[x >> 1][half][2 * (x & 1) + e] = z;
+      }
+  }
 }
 
 // Four channels of one row to the output, and its log-sum-exp. Weights were taken as
@@ -344,7 +367,7 @@ __device__ __forceinline__ void write_row(const PagedAttnParams& p, int b, int h
 }
 
 constexpr int kFewWarps = 4;
-constexpr int kFewWarpsAlone = 16;  // where one CTA takes all pages of a short sequence
+constexpr int kFewWarpsAlone = 12;  // where one CTA takes all pages of a short sequence
 
 template <int D, int ROWS, int WARPS>
 struct FewCfg {
@@ -353,7 +376,7 @@ struct FewCfg {
   static constexpr int SMEM = RING > JOIN ? RING : JOIN;
 };
 
-// Few rows: one CTA of 4 (or 16) warps per (split of the pages, 16- or 8-row tile, key head,
+// Few rows: one CTA of 4 (or 12) warps per (split of the pages, 16- or 8-row tile, key head,
 // sequence). Every warp walks 32-token units of codes on its own. Its own asynchronous
 // copies bring the next unit's K as soon as this one's scores are taken, and the next V as
 // soon as this one's products are: one buffer each, so that 16 warps fit an SM. (Between
@@ -377,10 +400,11 @@ __global__ void __launch_bounds__(WARPS * 32) paged_few_kernel(const __grid_cons
   const int b = bh / p.c.H, h = bh - b * p.c.H;
   const int row0 = tile * ROWS;
   const bool with_pos = MODE == kGeneral && p.c.pos;
+  const bool by_pos = with_pos && (p.first || (p.prefix && p.causal));  // positions decide what is seen
 
   const SeqView sv = seq_view(p, b);
   FewRowsView<ROWS> view;
-  view.load(p, sv, b, h, row0, lane, with_pos);
+  view.load(p, sv, b, h, row0, lane, by_pos);
   const int pg_lo = min(view.lo_min, view.hi_max) / kPage, pg_hi = (view.hi_max + kPage - 1) / kPage;
   const int per = (pg_hi - pg_lo + p.splits - 1) / p.splits;
   const int pg0 = pg_lo + split * per, pg1 = min(pg_hi, pg0 + per);
@@ -647,6 +671,7 @@ __global__ void __launch_bounds__(kFewWarps * 32) paged_weights_kernel(const __g
   const int bh = blockIdx.x / p.splits;
   const int b = bh / p.c.H, h = bh - b * p.c.H;
   const bool with_pos = MODE == kGeneral && p.c.pos;
+  const bool by_pos = with_pos && (p.first || (p.prefix && p.causal));  // positions decide what is seen
   const SeqView sv = seq_view(p, b);
   const int pages = (sv.len + kPage - 1) / kPage;
   const int per = (pages + p.splits - 1) / p.splits;
@@ -673,7 +698,7 @@ __global__ void __launch_bounds__(kFewWarps * 32) paged_weights_kernel(const __g
       copy_commit();
     }
     FewRowsView<ROWS> view;
-    view.load(p, sv, b, h, row0, lane, with_pos);
+    view.load(p, sv, b, h, row0, lane, by_pos);
     uint32_t qb[KS][ROWS / 4];
     float back[NH][2], base[NH][2];
     load_q<D, ROWS>(p, sv, b, h, row0, lane, qb, back);

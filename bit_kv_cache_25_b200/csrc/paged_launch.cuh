@@ -12,7 +12,7 @@ struct PagedPlan {
   int rows, row_tiles, splits, warps;
 };
 
-// Up to so many pages a CTA of 16 warps takes a sequence whole where CTAs are few: no join after it.
+// Up to so many pages a CTA of 12 warps takes a sequence whole where CTAs are few: no join after it.
 constexpr int kAlonePages = 32;
 constexpr int kFewRows = 32;  // at most so many rows per key head take the few-row kernels
 

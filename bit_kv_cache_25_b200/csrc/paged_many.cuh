@@ -38,15 +38,15 @@ struct ManyCfg {
   static constexpr int Q0 = 0;
   static constexpr int K0 = 2 * TILE;
   static constexpr int V0 = K0 + 2 * TILE;
-  static constexpr int HDR0 = V0 + 2 * TILE;  // 4 x {8 floats, 128 positions}
-  static constexpr int HDR = 32 + 128 * 4;
+  static constexpr int HDR0 = V0 + 2 * TILE;  // 4 x {8 floats, 128 x {position, the same from the first query's, float32}}
+  static constexpr int HDR = 32 + 128 * 8;
   static constexpr int BARS = HDR0 + 4 * HDR;
   static constexpr int NBARS = 18;
   static constexpr int TMEM_SLOT = BARS + NBARS * 8;
   static constexpr int V0_SLOT = TMEM_SLOT + 8;
   static constexpr int SMEM = V0_SLOT + 8;
   static constexpr int SMEM_ALLOC = SMEM + 1024;
-  static constexpr int THREADS = 512;  // 128 registers each at launch, shared out below: 256 x 168 + 128 x 80 + 128 x 96
+  static constexpr int THREADS = 512;  // 128 registers each at launch, shared out below: 256 x 152 + 128 x 80 + 128 x 128
   static constexpr int COL_O = 128;  // tile qt: columns 256 * qt: scores [0, 128), output [128, 128 + D)
   static_assert(SMEM_ALLOC <= 232448 && TILE % 1024 == 0, "shared memory");
 };
@@ -117,10 +117,22 @@ __device__ __forceinline__ void store_codes(const uint4& x, uint32_t at) {
   tc::sts128(at ^ 16u, y[4], y[5], y[6], y[7]);
 }
 
+// Query i and head g (of its key head's) of a row, and of rows a fixed step further on, without a division for each.
+struct RowWalk {
+  int i, g, di, dg;
+  __device__ __forceinline__ RowWalk(const PagedAttnParams& p, int row, int step)
+      : i(row / p.G), g(row % p.G), di(step / p.G), dg(step % p.G) {}
+  __device__ __forceinline__ void next(const PagedAttnParams& p) {
+    i += di;
+    g += dg;
+    if (g >= p.G) g -= p.G, ++i;
+  }
+};
+
 struct ManyRow {
-  int lo, hi;   // slots seen (general mode: hi is the causal bound, lo unused)
-  int first, pos, prefix;
-  float slope;
+  int lo, hi;  // slots seen (where positions decide: hi is the causal bound, lo unused)
+  int first, prefix;
+  float pos, slope;
   bool live;
 };
 
@@ -155,6 +167,23 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1) paged_many_kernel(cons
   if (row0 >= rows) return;  // (uniform: no live row)
   const int nq = rows - row0 > 128 ? 2 : 1;
 
+  // the query rows into their K-major tiles as they are, whole rows at a time, by all warps; what follows hides their way
+  {
+    constexpr int CPR = D / 8, RPI = 512 / CPR;  // 16-byte chunks per row, rows per pass of the CTA
+    const int c = tid % CPR;
+    const uint16_t* q = p.q + b * p.q_sb + static_cast<int64_t>(h) * p.G * p.q_sh + c * 8;
+    RowWalk at(p, row0 + tid / CPR, RPI);
+    int r = tid / CPR;
+#pragma unroll 4
+    for (int x = 0; x < 256 / RPI; ++x, r += RPI, at.next(p)) {
+      const bool live = at.i < sv.q_len;
+      copy16_or_zero(sbase + C::Q0 + (r >> 7) * C::TILE + (c >> 3) * (128 * 128) + ((r & 127) >> 3) * 1024 + (r & 7) * 128 +
+                         (((c & 7) ^ (r & 7)) << 4),
+                     q + (live ? at.g * p.q_sh + at.i * p.q_st : 0), live);
+    }
+    copy_commit();
+  }
+
   // ---- set-up
   if (warp == 15) {
     tc::tmem_alloc(tmem_slot, 512);
@@ -178,6 +207,8 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1) paged_many_kernel(cons
     *v0_slot = 1.0f;
   }
   __syncthreads();
+  const bool with_pos = MODE == kGeneral && p.c.pos;
+  const bool by_pos = with_pos && (p.first || (p.prefix && p.causal));  // positions decide what is seen
   ManyRow rv{};
   if (tid < 256) {
     const RowView r = row_view(p, sv, b, h, row0 + tid);
@@ -186,16 +217,8 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1) paged_many_kernel(cons
     rv.pos = r.pos;
     rv.slope = r.slope;
     rv.prefix = p.causal && p.prefix ? sv.prefix : INT32_MIN;
-    rv.lo = 0;
-    rv.hi = max(r.hi, 0);
-    int reach = rv.hi;
-    if (rv.live && p.causal && p.prefix) {
-      if (MODE == kGeneral && p.c.pos)
-        reach = sv.len;
-      else
-        reach = rv.hi = max(rv.hi, min(sv.len, sv.prefix));
-    }
-    if (!(MODE == kGeneral && p.c.pos) && rv.live) rv.lo = max(rv.first, 0);
+    row_interval(p, sv, r, by_pos, rv.lo, rv.hi);
+    const int reach = by_pos && rv.live && p.causal && p.prefix ? sv.len : rv.hi;
     int lo = rv.live ? rv.lo : INT32_MAX;
     int hi = rv.live ? reach : 0;
     if (lo >= hi) lo = INT32_MAX, hi = 0;
@@ -206,6 +229,8 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1) paged_many_kernel(cons
       atomicMax(&range[1], hi);
     }
   }
+  copy_wait<0>();
+  fence_proxy_async_smem();
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
@@ -224,77 +249,75 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1) paged_many_kernel(cons
     // nothing to see: the rows are written below
   } else if (warp < 8) {
     // ================================================================ softmax
-    set_registers<168>();
+    set_registers<152>();
     const int qt = warp >> 2;
     if (qt < nq) {
       const uint32_t lane_tm = tm + (static_cast<uint32_t>((warp & 3) * 32) << 16) + qt * 256;
       float back = 1.0f;
-      {  // this thread's query row into the K-major tile
-        const int row = row0 + tid;
-        const int i = row / p.G, hq = h * p.G + row % p.G;
-        const uint4* q = reinterpret_cast<const uint4*>(p.q + b * p.q_sb + hq * p.q_sh + i * p.q_st);
-        uint4 v[D / 8];
-        uint32_t top = 0;
-#pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-          v[c] = rv.live ? __ldg(q + c) : make_uint4(0, 0, 0, 0);
-          top = __vmaxu2(top, __vmaxu2(__vmaxu2(v[c].x & 0x7fff7fffu, v[c].y & 0x7fff7fffu),
-                                       __vmaxu2(v[c].z & 0x7fff7fffu, v[c].w & 0x7fff7fffu)));
-        }
-        float f = 1.0f;
+      {  // bf16 rows to fp16 in place
+        constexpr int CPR = D / 8, RPI = 32 / CPR, N = 32 / RPI;  // 16-byte chunks per row, rows at a time, turns
+        constexpr int U = 4;
+        const int c = lane % CPR;
         if (p.q_bf16) {
-          top = max(top & 0xffffu, top >> 16);
-          const int e = max(min(static_cast<int>(top >> 7) - 127, 119), -119);
-          f = __uint_as_float(static_cast<uint32_t>(127 + 7 - e) << 23);
-          back = __uint_as_float(static_cast<uint32_t>(127 - 7 + e) << 23);
-        }
-        const int r = tid & 127;
-        const uint32_t at = sbase + C::Q0 + qt * C::TILE + (r >> 3) * 1024 + (r & 7) * 128;
+#pragma unroll 1
+          for (int x0 = 0; x0 < N; x0 += U) {
+            uint4 v[U];
+            uint32_t top[U], place[U];
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-          if (p.q_bf16) {
+            for (int x = 0; x < U; ++x) {
+              const int r = (warp & 3) * 32 + (x0 + x) * RPI + lane / CPR;
+              place[x] = C::Q0 + qt * C::TILE + (c >> 3) * (128 * 128) + (r >> 3) * 1024 + (r & 7) * 128 + (((c & 7) ^ (r & 7)) << 4);
+              v[x] = lds128(sm + place[x]);
+            }
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              const uint32_t x = (&v[c].x)[w];
-              (&v[c].x)[w] = tc::cvt_half2(__uint_as_float(x << 16) * f, __uint_as_float(x & 0xffff0000u) * f);
+            for (int x = 0; x < U; ++x) {
+              const uint32_t m = __vmaxu2(__vmaxu2(v[x].x & 0x7fff7fffu, v[x].y & 0x7fff7fffu),
+                                          __vmaxu2(v[x].z & 0x7fff7fffu, v[x].w & 0x7fff7fffu));
+              top[x] = max(m & 0xffffu, m >> 16);
+            }
+#pragma unroll
+            for (int o = 1; o < CPR; o <<= 1)
+#pragma unroll
+              for (int x = 0; x < U; ++x) top[x] = max(top[x], __shfl_xor_sync(0xffffffffu, top[x], o));
+#pragma unroll
+            for (int x = 0; x < U; ++x) {
+              const int e = max(min(static_cast<int>(top[x] >> 7) - 127, 119), -119);
+              const float f = __uint_as_float(static_cast<uint32_t>(127 + 7 - e) << 23);
+              const int e_mine = __shfl_sync(0xffffffffu, e, (lane % RPI) * CPR);  // of row (x0 + x) * RPI + lane % RPI
+              if (lane / RPI == x0 + x) back = __uint_as_float(static_cast<uint32_t>(127 - 7 + e_mine) << 23);
+#pragma unroll
+              for (int w = 0; w < 4; ++w) {
+                const uint32_t y = (&v[x].x)[w];
+                (&v[x].x)[w] = tc::cvt_half2(__uint_as_float(y << 16) * f, __uint_as_float(y & 0xffff0000u) * f);
+              }
+              tc::sts128(sbase + place[x], v[x].x, v[x].y, v[x].z, v[x].w);
             }
           }
-          tc::sts128(at + (c >> 3) * (128 * 128) + (((c & 7) ^ (r & 7)) << 4), v[c].x, v[c].y, v[c].z, v[c].w);
         }
         fence_proxy_async_smem();
         warp_arrive(q_full, lane);
       }
       const float fz = p.sigma * back * (MODE == kPlain ? kLog2e : 1.0f);
       const float cap_f = MODE != kPlain && p.cap > 0.0f ? 2.0f * kLog2e / p.cap : 0.0f;
+      const float over = MODE != kPlain && p.cap > 0.0f ? 1.0f / p.cap : 0.0f;
       for (int j = 0; j < T; ++j) {
         const int slot0 = (t0 + j) * C::KT;
         ok = mbar_wait_warp(&h_full[j & 3], (j >> 2) & 1) && mbar_wait_warp(&s_full[qt], j & 1);
         if (!ok) break;
         tc::fence_after_sync();
         const float* hdr = reinterpret_cast<const float*>(sm + C::HDR0 + (j & 3) * C::HDR);
-        const int* kp = reinterpret_cast<const int*>(hdr + 8);
-        const bool with_pos = MODE == kGeneral && p.c.pos;
+        const int2* kp = reinterpret_cast<const int2*>(hdr + 8);
         const int lo = rv.lo - slot0, hi = rv.hi - slot0;
-        const bool whole = __all_sync(0xffffffffu, lo <= 0 && hi >= C::KT) && !with_pos;
+        const bool whole = __all_sync(0xffffffffu, lo <= 0 && hi >= C::KT) && !by_pos;
         // (a page of zero scale still gives -inf where masked)
         const float f0 = fmaxf(hdr[0] * fz, 1e-37f), f1 = fmaxf(hdr[1] * fz, 1e-37f);
+        const float slot_f = static_cast<float>(slot0 - sv.pos0);
         auto seen = [&](int col) {
-          if (with_pos) {
-            const int k = kp[col];
+          if (by_pos) {
+            const int k = kp[col].x;
             return rv.live && slot0 + col < sv.len && (col < hi || k < rv.prefix) && k >= rv.first;
           }
           return col >= lo && col < hi;
-        };
-        // a score in log2 units, without the mask
-        auto score = [&](float a, float f, int col) {
-          float z = a * f;
-          if (MODE == kPlain) return z;
-          z = MODE == kCap || p.cap > 0.0f ? capped(z, p.cap, cap_f) : z * kLog2e;
-          if (MODE == kGeneral) {
-            const int k = p.c.pos ? kp[col] : slot0 + col;
-            z = fmaf(-rv.slope, fabsf(static_cast<float>(rv.pos - k)), z);
-          }
-          return z;
         };
         float xs[2][64];
         tmem_ld32(lane_tm, xs[0]);
@@ -305,9 +328,34 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1) paged_many_kernel(cons
           const float f = half ? f1 : f0, lc = hdr[2 + half];
           float(&x)[64] = xs[half];
           tc::tmem_wait_ld();
-          if (MODE != kPlain) {
+          if (MODE == kCap || (MODE == kGeneral && p.cap > 0.0f)) {
+            float m4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int i = 0; i < 64; ++i) x[i] = score(x[i], f, c0 + i);
+            for (int i = 0; i < 64; i += 8)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) m4[k] = tc::max3(m4[k], fabsf(x[i + 2 * k]), fabsf(x[i + 2 * k + 1]));
+            const float most = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+            if (__all_sync(0xffffffffu, most * f <= kCapSmall * p.cap)) {
+              const float fc = f * over, cl = p.cap * kLog2e;
+#pragma unroll
+              for (int i = 0; i < 64; ++i) x[i] = capped_small(x[i], fc, cl);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 64; ++i) x[i] = capped(x[i] * f, p.cap, cap_f);
+            }
+          } else if (MODE == kGeneral) {
+#pragma unroll
+            for (int i = 0; i < 64; ++i) x[i] *= f * kLog2e;
+          }
+          if (MODE == kGeneral) {
+            if (with_pos) {
+#pragma unroll
+              for (int i = 0; i < 64; ++i) x[i] = fmaf(-rv.slope, fabsf(rv.pos - __int_as_float(kp[c0 + i].y)), x[i]);
+            } else {
+              const float from = rv.pos - slot_f;
+#pragma unroll
+              for (int i = 0; i < 64; ++i) x[i] = fmaf(-rv.slope, fabsf(from - static_cast<float>(c0 + i)), x[i]);
+            }
           }
           if (!whole) {
 #pragma unroll
@@ -409,7 +457,7 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1) paged_many_kernel(cons
           vs[i] = ph[i] < 0 ? -1.0f : __ldg(p.c.scale[1] + ph[i]);
         }
       }
-      if (MODE == kGeneral && p.c.pos) pos = ph[u >> 6] < 0 ? 0 : __ldg(p.c.pos + ph[u >> 6] * kPage + (u & 63));
+      if (with_pos) pos = ph[u >> 6] < 0 ? 0 : __ldg(p.c.pos + ph[u >> 6] * kPage + (u & 63));
     };
     load(0);
     for (int j = 0; j < T; ++j) {
@@ -435,51 +483,15 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1) paged_many_kernel(cons
           hdr[4 + i] = inv;
         }
       }
-      if (MODE == kGeneral && p.c.pos) reinterpret_cast<int*>(hdr + 8)[u] = pos;
+      if (with_pos) reinterpret_cast<int2*>(hdr + 8)[u] = make_int2(pos, __float_as_int(static_cast<float>(pos - sv.pos0)));
       fence_proxy_async_smem();
       warp_arrive(&k_full[j & 1], lane);
       if (lane == 0) mbar_arrive(&h_full[j & 3]);
       if (j + 1 < T) load(j + 1);
     }
-  } else if (warp < 15) {
-    // =============================================================== unpack V
-    set_registers<96>();
-    // the three warps take the tile's warp loads (RPW rows each) in turn
-    constexpr int RPW = 512 / D, LOADS = 128 / RPW, N = (LOADS + 2) / 3;
-    int r0, g;
-    unpack_lane<D>(lane, r0, g);
-    const int w = warp - 12;
-    const int from = r0 * D + g * 16;
-    uint4 x[N];
-    int64_t ph[2];
-    auto load = [&](int j) {
-      many_pages(p, sv, b, h, (t0 + j) * 2, ph);
-      const unsigned char* src0 = p.c.code[1] + ph[0] * (kPage * D) + from;
-      const unsigned char* src1 = p.c.code[1] + (ph[1] - 1) * (kPage * D) + from;  // rows 64 .. 127
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const int q = 3 * i + w;  // (warp-uniform)
-        const bool late = q >= LOADS / 2;
-        x[i] = make_uint4(0, 0, 0, 0);
-        if (q < LOADS && ph[late] >= 0) x[i] = __ldg(reinterpret_cast<const uint4*>((late ? src1 : src0) + q * (RPW * D)));
-      }
-    };
-    load(0);
-    for (int j = 0; j < T; ++j) {
-      if (j >= 2 && !(ok = mbar_wait_warp(&v_empty[j & 1], ((j >> 1) - 1) & 1))) break;
-      const uint32_t to = sbase + C::V0 + (j & 1) * C::TILE;
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const int q = 3 * i + w;
-        if (q < LOADS) store_codes<CODE>(x[i], to + unpack_at(q * RPW + r0, g));
-      }
-      fence_proxy_async_smem();
-      warp_arrive(&v_full[j & 1], lane);
-      if (j + 1 < T) load(j + 1);
-    }
   } else {
+    if (warp == 15) {
     // ==================================================================== MMA
-    set_registers<96>();
     const uint32_t idesc_qk = tc::idesc_f16_f32(128, 128);
     const uint32_t idesc_pv = tc::idesc_f16_f32(128, D, /*b_mn_major=*/true);
     const uint64_t qd = tc::sw128_desc(sbase + C::Q0);
@@ -528,6 +540,42 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1) paged_many_kernel(cons
       pv(1, (T - 1) & 1, T == 1);
     }
     if (ok) tc::commit_warp(o_full);
+    } else {
+    // =============================================================== unpack V
+    // the three warps take the tile's warp loads (RPW rows each) in turn
+    constexpr int RPW = 512 / D, LOADS = 128 / RPW, N = (LOADS + 2) / 3;
+    int r0, g;
+    unpack_lane<D>(lane, r0, g);
+    const int w = warp - 12;
+    const int from = r0 * D + g * 16;
+    uint4 x[N];
+    int64_t ph[2];
+    auto load = [&](int j) {
+      many_pages(p, sv, b, h, (t0 + j) * 2, ph);
+      const unsigned char* src0 = p.c.code[1] + ph[0] * (kPage * D) + from;
+      const unsigned char* src1 = p.c.code[1] + (ph[1] - 1) * (kPage * D) + from;  // rows 64 .. 127
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int q = 3 * i + w;  // (warp-uniform)
+        const bool late = q >= LOADS / 2;
+        x[i] = make_uint4(0, 0, 0, 0);
+        if (q < LOADS && ph[late] >= 0) x[i] = __ldg(reinterpret_cast<const uint4*>((late ? src1 : src0) + q * (RPW * D)));
+      }
+    };
+    load(0);
+    for (int j = 0; j < T; ++j) {
+      if (j >= 2 && !(ok = mbar_wait_warp(&v_empty[j & 1], ((j >> 1) - 1) & 1))) break;
+      const uint32_t to = sbase + C::V0 + (j & 1) * C::TILE;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int q = 3 * i + w;
+        if (q < LOADS) store_codes<CODE>(x[i], to + unpack_at(q * RPW + r0, g));
+      }
+      fence_proxy_async_smem();
+      warp_arrive(&v_full[j & 1], lane);
+      if (j + 1 < T) load(j + 1);
+    }
+    }
   }
 
   // ---- output: one row per thread
@@ -543,35 +591,52 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1) paged_many_kernel(cons
     const float v0 = *v0_slot * code_unit<CODE>();
     const float inv = part ? v0 : (l == 0.0f ? 0.0f : __fdiv_rn(v0, l));
     const int64_t pr = (static_cast<int64_t>(split) * p.B * p.c.H + bh) * (static_cast<int64_t>(p.row_tiles) * 256) + row;
+    // through the query tile's place in shared memory (its last product is done), to be stored as whole rows
+    const uint32_t stage = sbase + C::Q0 + (warp >> 2) * C::TILE + ((tid & 127) >> 3) * 1024 + (tid & 7) * 128;
 #pragma unroll 1
-    for (int c = 0; ok && c < D; c += 16) {
-      uint32_t o[16];
+    for (int c = 0; ok && c < D; c += 32) {
+      float v[32];
       if (T > 0) {
-        tc::tmem_ld16(lane_tm + c, o);
+        tmem_ld32(lane_tm + c, v);
         tc::tmem_wait_ld();
       } else {
 #pragma unroll
-        for (int x = 0; x < 16; ++x) o[x] = 0;
+        for (int x = 0; x < 32; ++x) v[x] = 0.0f;
       }
-      float v[16];
 #pragma unroll
-      for (int x = 0; x < 16; ++x) v[x] = __uint_as_float(o[x]) * inv;
-      if (!rv.live) {
-        // a row of no query is left as it is
-      } else if (part) {
+      for (int x = 0; x < 32; ++x) v[x] *= inv;
+      if (part) {
+        if (rv.live) {
 #pragma unroll
-        for (int x = 0; x < 16; x += 4)
-          *reinterpret_cast<float4*>(p.part_o + pr * D + c + x) = make_float4(v[x], v[x + 1], v[x + 2], v[x + 3]);
+          for (int x = 0; x < 32; x += 4)
+            *reinterpret_cast<float4*>(p.part_o + pr * D + c + x) = make_float4(v[x], v[x + 1], v[x + 2], v[x + 3]);
+        }
       } else {
-        uint32_t w[8];
 #pragma unroll
-        for (int x = 0; x < 8; ++x)
-          w[x] = p.q_bf16 ? tc::cvt_bf162(v[2 * x], v[2 * x + 1]) : tc::cvt_half2(v[2 * x], v[2 * x + 1]);
-        uint4* out = reinterpret_cast<uint4*>(p.out + b * p.o_sb + hq * p.o_sh + i * p.o_st + c);
-        out[0] = make_uint4(w[0], w[1], w[2], w[3]);
-        out[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        for (int x = 0; x < 4; ++x) {
+          uint32_t w[4];
+#pragma unroll
+          for (int y = 0; y < 4; ++y)
+            w[y] = p.q_bf16 ? tc::cvt_bf162(v[8 * x + 2 * y], v[8 * x + 2 * y + 1]) : tc::cvt_half2(v[8 * x + 2 * y], v[8 * x + 2 * y + 1]);
+          const int chunk = c / 8 + x;
+          tc::sts128(stage + (chunk >> 3) * (128 * 128) + (((chunk & 7) ^ (tid & 7)) << 4), w[0], w[1], w[2], w[3]);
+        }
       }
       __syncwarp();
+    }
+    if (ok && !part) {
+      constexpr int CPR = D / 8, RPI = 32 / CPR;
+      const int c = lane % CPR;
+      const unsigned char* from = sm + C::Q0 + (warp >> 2) * C::TILE + (c >> 3) * (128 * 128);
+      RowWalk at(p, row0 + warp * 32 + lane / CPR, RPI);
+      uint16_t* out = p.out + b * p.o_sb + static_cast<int64_t>(h) * p.G * p.o_sh + c * 8;
+#pragma unroll 4
+      for (int x = 0; x < 32 / RPI; ++x, at.next(p)) {
+        const int r = (warp & 3) * 32 + x * RPI + lane / CPR;
+        if (at.i < sv.q_len)  // (a row of no query is left as it is)
+          *reinterpret_cast<uint4*>(out + at.g * p.o_sh + at.i * p.o_st) =
+              lds128(from + (r >> 3) * 1024 + (r & 7) * 128 + (((c & 7) ^ (r & 7)) << 4));
+      }
     }
     if (ok && rv.live) {
       if (part)

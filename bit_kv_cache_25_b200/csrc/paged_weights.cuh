@@ -42,10 +42,11 @@ struct SumCfg {
   static constexpr int TILE = 128 * D * 2;
   static constexpr int K0 = 0;
   static constexpr int Q0 = TILE;               // ring of two
-  static constexpr int META0 = 3 * TILE;        // ring of four SumRows
-  static constexpr int META = 128 * 28;
-  static constexpr int BARS = META0 + 4 * META;
-  static constexpr int NBARS = 12;
+  static constexpr int META0 = 3 * TILE;        // ring of five SumRows
+  static constexpr int META = 128 * 20 + 16;
+  static constexpr int AT0 = META0 + 5 * META;  // the rows' places in q, in elements, -1: none (two tiles)
+  static constexpr int BARS = AT0 + 2 * 128 * 8;
+  static constexpr int NBARS = 13;
   static constexpr int TMEM_SLOT = BARS + NBARS * 8;
   static constexpr int SMEM = TMEM_SLOT + 16;
   static constexpr int SMEM_ALLOC = SMEM + 1024;
@@ -57,10 +58,10 @@ struct SumCfg {
 struct SumRows {
   float lse[128];   // log2 units; +inf: no weight
   float slope[128];
-  int hi[128];      // slots seen are [lo, hi) (with positions: hi the causal bound, lo the first position)
+  int hi[128];      // slots seen are [lo, hi) (where positions decide: hi the causal bound, lo the first position)
   int lo[128];
-  int pos[128];
-  int64_t at[128];  // of the row in q, in elements; -1: none
+  float pos[128];   // from the first query's
+  int whole[4];     // whether every row of 32 sees the whole key tile
 };
 
 template <int D, int CODE, int MODE>
@@ -88,6 +89,7 @@ __global__ void __launch_bounds__(SumCfg<D>::THREADS, 2) paged_sums_kernel(const
   many_pages(p, sv, b, h, slot0 / kPage, ph);
   const int rows = sv.q_len * p.G;
   const bool with_pos = MODE == kGeneral && p.c.pos;
+  const bool by_pos = with_pos && (p.first || (p.prefix && p.causal));  // positions decide what is seen
   int rt0 = 0;
   // row tiles that end before the causal rule lets any of their rows see this tile (a prefix may let every row)
   if (p.causal && !(p.prefix && (p.c.pos || slot0 < sv.prefix)))
@@ -105,7 +107,7 @@ __global__ void __launch_bounds__(SumCfg<D>::THREADS, 2) paged_sums_kernel(const
       mbar_init(&s_full[i], 1);
       mbar_init(&s_empty[i], 4);
     }
-    for (int i = 0; i < 4; ++i) mbar_init(&m_full[i], 4);
+    for (int i = 0; i < 5; ++i) mbar_init(&m_full[i], 4);
     fence_barrier_init();
   }
   if (warp < 8) {  // K, once
@@ -147,22 +149,21 @@ __global__ void __launch_bounds__(SumCfg<D>::THREADS, 2) paged_sums_kernel(const
     const float f = a < 0 ? 0.0f : __ldg(p.c.scale[0] + a) * p.sigma * unit * (MODE == kPlain ? kLog2e : 1.0f);
     const float cap_f = MODE != kPlain && p.cap > 0.0f ? 2.0f * kLog2e / p.cap : 0.0f;
     const int kp = with_pos ? (key ? __ldg(p.c.pos + a * kPage + (tid & 63)) : 0) : slot;
+    const float kf = static_cast<float>(kp - sv.pos0);
+    const bool cap = MODE == kCap || (MODE == kGeneral && p.cap > 0.0f);
+    const float over = cap ? 1.0f / p.cap : 0.0f;
     const uint32_t lane_tm = tm + (static_cast<uint32_t>(warp * 32) << 16);
     const int prefix = p.causal && p.prefix ? sv.prefix : INT32_MIN;
     float w = 0.0f;
+    int slot_m = 0, turn_m = 0;  // ring of five: slot, and the parity of its use
     for (int j = 0; j < T; ++j) {
-      ok = mbar_wait_warp(&m_full[j & 3], (j >> 2) & 1) && mbar_wait_warp(&s_full[j & 1], (j >> 1) & 1);
+      ok = mbar_wait_warp(&m_full[slot_m], turn_m) && mbar_wait_warp(&s_full[j & 1], (j >> 1) & 1);
       if (!ok) break;
       tc::fence_after_sync();
-      const SumRows& meta = *reinterpret_cast<const SumRows*>(sm + C::META0 + (j & 3) * C::META);
-      // whether every row of the tile sees every key of the warp
-      bool whole = !with_pos;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = i * 32 + lane;
-        whole &= meta.lse[r] == INFINITY || (meta.lo[r] <= slot0 && meta.hi[r] >= slot0 + 128);
-      }
-      whole = __all_sync(0xffffffffu, whole);
+      const SumRows& meta = *reinterpret_cast<const SumRows*>(sm + C::META0 + slot_m * C::META);
+      if (++slot_m == 5) slot_m = 0, turn_m ^= 1;
+      const int4 whole4 = *reinterpret_cast<const int4*>(meta.whole);
+      const bool whole = whole4.x & whole4.y & whole4.z & whole4.w;
       float sum0 = 0.0f, sum1 = 0.0f;
 #pragma unroll 1
       for (int c0 = 0; c0 < 128; c0 += 32) {
@@ -172,17 +173,37 @@ __global__ void __launch_bounds__(SumCfg<D>::THREADS, 2) paged_sums_kernel(const
 #pragma unroll
         for (int i = 0; i < 8; ++i) ls[i] = *reinterpret_cast<const float4*>(&meta.lse[c0 + 4 * i]);
         tc::tmem_wait_ld();
+        bool small = false;
+        if (cap) {
+          float m0 = 0.0f, m1 = 0.0f;
+#pragma unroll
+          for (int i = 0; i < 32; i += 4) {
+            m0 = tc::max3(m0, fabsf(x[i]), fabsf(x[i + 1]));
+            m1 = tc::max3(m1, fabsf(x[i + 2]), fabsf(x[i + 3]));
+          }
+          small = __all_sync(0xffffffffu, fmaxf(m0, m1) * f <= kCapSmall * p.cap);
+        }
+        if (MODE != kPlain) {
+          if (small) {
+            const float fc = f * over, cl = p.cap * kLog2e;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[i] = capped_small(x[i], fc, cl);
+          } else if (cap) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[i] = capped(x[i] * f, p.cap, cap_f);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[i] *= f * kLog2e;
+          }
+        }
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
-          float z = x[i] * f;
-          if (MODE != kPlain) {
-            z = MODE == kCap || p.cap > 0.0f ? capped(z, p.cap, cap_f) : z * kLog2e;
-            if (MODE == kGeneral) z = fmaf(-meta.slope[c0 + i], fabsf(static_cast<float>(meta.pos[c0 + i] - kp)), z);
-          }
+          float z = MODE == kPlain ? x[i] * f : x[i];
+          if (MODE == kGeneral) z = fmaf(-meta.slope[c0 + i], fabsf(meta.pos[c0 + i] - kf), z);
           z -= (&ls[i >> 2].x)[i & 3];
           if (!whole) {
             const int hi = meta.hi[c0 + i], lo = meta.lo[c0 + i];
-            const bool see = with_pos ? (slot < hi || kp < prefix) && kp >= lo : slot < hi && slot >= lo;
+            const bool see = by_pos ? (slot < hi || kp < prefix) && kp >= lo : slot < hi && slot >= lo;
             z = see ? z : -INFINITY;
           }
           const float e = tc::ex2(z);
@@ -208,42 +229,57 @@ __global__ void __launch_bounds__(SumCfg<D>::THREADS, 2) paged_sums_kernel(const
       fence_proxy_async_smem();
       warp_arrive(&q_full[j & 1], lane);
     };
+    int64_t* ats = reinterpret_cast<int64_t*>(sm + C::AT0);
+    // what this thread's row of a tile sees, loaded a tile ahead
+    RowView v;
+    int64_t at;
+    float lse;
+    auto look = [&](int j) {
+      const int row = (rt0 + j) * 128 + u;
+      v = row_view(p, sv, b, h, row);
+      at = -1;
+      lse = -INFINITY;
+      if (v.hi >= 0) {
+        const int i = row / p.G, hq = h * p.G + row % p.G;
+        at = b * p.q_sb + hq * p.q_sh + i * p.q_st;
+        lse = __ldg(p.lse + (static_cast<int64_t>(b) * p.Hq + hq) * p.n + i);
+      }
+    };
+    if (T > 0) look(0);
+    int slot_m = 0;
     for (int j = 0; j < T; ++j) {
-      // (after a wait that gave up, the four warps still meet at every barrier below)
-      if (ok && j >= 2) ok = mbar_wait_warp(&q_empty[j & 1], ((j >> 1) - 1) & 1);
-      // (the slot of the ring of four was last read with the scores of tile j - 4, which the products of tile j - 2 follow)
-      SumRows& meta = *reinterpret_cast<SumRows*>(sm + C::META0 + (j & 3) * C::META);
+      // (after a wait that gave up, the four warps still meet at every barrier below; the ring's slot was last read with
+      // the scores of tile j - 5, and the products of tile j - 3, waited for a turn ago, follow those)
+      SumRows& meta = *reinterpret_cast<SumRows*>(sm + C::META0 + slot_m * C::META);
+      uint64_t* full_m = &m_full[slot_m];
+      if (++slot_m == 5) slot_m = 0;
       {
-        const int row = (rt0 + j) * 128 + u;
-        const RowView v = row_view(p, sv, b, h, row);
-        float lse = INFINITY;
-        int64_t at = -1;
-        int hi = max(v.hi, 0);
-        if (v.hi >= 0) {
-          const int i = row / p.G, hq = h * p.G + row % p.G;
-          at = b * p.q_sb + hq * p.q_sh + i * p.q_st;
-          const float x = __ldg(p.lse + (static_cast<int64_t>(b) * p.Hq + hq) * p.n + i);
-          if (x != -INFINITY) lse = x * kLog2e;
-          if (p.causal && p.prefix && !with_pos) hi = max(hi, min(sv.len, sv.prefix));
-        }
-        meta.lse[u] = lse;
+        int lo, hi;
+        row_interval(p, sv, v, by_pos, lo, hi);
+        if (by_pos) lo = v.first;
+        const bool none = v.hi < 0 || lse == -INFINITY;
+        meta.lse[u] = none ? INFINITY : lse * kLog2e;
         meta.slope[u] = v.slope;
         meta.hi[u] = hi;
-        meta.lo[u] = with_pos ? v.first : max(v.first, 0);
+        meta.lo[u] = lo;
         meta.pos[u] = v.pos;
-        meta.at[u] = at;
+        ats[(j & 1) * 128 + u] = at;
+        const bool all = __all_sync(0xffffffffu, none || (!by_pos && lo <= slot0 && hi >= slot0 + 128));
+        if (lane == 0) meta.whole[warp - 4] = all;
       }
       asm volatile("bar.sync 1, 128;" ::: "memory");
       if (!ok) continue;
-      warp_arrive(&m_full[j & 3], lane);
+      warp_arrive(full_m, lane);
+      if (j + 1 < T) look(j + 1);
+      if (j >= 2 && !(ok = mbar_wait_warp(&q_empty[j & 1], ((j >> 1) - 1) & 1))) continue;
       const int c = u % CPR;
       const uint32_t to = sbase + C::Q0 + (j & 1) * C::TILE + (c >> 3) * (128 * 128);
 #pragma unroll
       for (int i = 0; i < 128 / RPI; ++i) {
         const int row = i * RPI + u / CPR;
-        const int64_t at = meta.at[row];
+        const int64_t at = ats[(j & 1) * 128 + row];
         copy16_or_zero(to + (row >> 3) * 1024 + (row & 7) * 128 + (((c & 7) ^ (row & 7)) << 4),
-                   p.q + (at < 0 ? 0 : at + c * 8), at >= 0);
+                       p.q + (at < 0 ? 0 : at + c * 8), at >= 0);
       }
       copy_commit();
       if (j > 0) {

@@ -153,13 +153,13 @@ class Paged:
         for b in range(B):
             assert (got[b, :, ql[b]:] == 77.0).all() and (glse[b, :, ql[b]:] == 55.0).all()
         assert (room[:, n:] == 77.0).all() and (room[:, :, Hq:] == 77.0).all()
-        bad = np.abs(got - want) > tol
+        bad = ~(np.abs(got - want) <= tol)
         bad &= np.broadcast_to(live[..., None], bad.shape)
-        assert not bad.any(), (np.abs(got - want) / np.maximum(tol, 1e-300))[bad].max()
+        assert not bad.any(), ((np.abs(got - want) / np.maximum(tol, 1e-300))[bad].max(), np.argwhere(bad)[:4].tolist(), bad.sum())
         seen = np.isfinite(wlse)
         livef = np.broadcast_to(live, seen.shape)
         assert np.array_equal(np.isneginf(glse) & livef, ~seen & livef)
-        assert (np.abs(np.where(seen & livef, glse - np.where(seen, wlse, 0), 0)) <= ltol).all()
+        assert (np.abs(np.where(seen & livef, glse - np.where(seen, wlse, 0), 0)) <= ltol).all(), "lse"
         if self.o["weight"] is not None:
             before = self.o["weight"].copy()
             for acc in (False, True):
