@@ -459,6 +459,7 @@ __global__ void __launch_bounds__(WARPS * 32) paged_few_kernel(const __grid_cons
     __syncwarp();  // every lane has left K
     if (ph >= 0) copy_unit<D, 0>(p.c, ph, u & 1, k_at, lane, with_pos);  // (units of a warp are all first or all second halves)
     copy_commit();
+    __syncwarp();  // (some lanes copied the scales: the matrix instructions below want the warp as one)
     if (!there) {
       if (ph >= 0) copy_unit<D, 1>(p.c, ph, u & 1, v_at, lane, false);
       copy_commit();
@@ -720,6 +721,7 @@ __global__ void __launch_bounds__(kFewWarps * 32) paged_weights_kernel(const __g
       if (ph[kSumStages - 1] >= 0)
         copy_unit<D, 0>(p.c, ph[kSumStages - 1], u & 1, ring + (stage == 0 ? kSumStages - 1 : stage - 1) * UnitCfg<D>::K, lane, with_pos);
       copy_commit();
+      __syncwarp();  // (some lanes copied the scales: the matrix instructions below want the warp as one)
       const int64_t at_page = ph[0];
 #pragma unroll
       for (int i = 0; i < kSumStages - 1; ++i) ph[i] = ph[i + 1];

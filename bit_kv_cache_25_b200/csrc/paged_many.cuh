@@ -400,6 +400,7 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1) paged_many_kernel(cons
               }
             }
           }
+          __syncwarp();  // (tensor memory wants the warp as one)
           const float off = lc - (R == -INFINITY ? 0.0f : R) + 7.0f;
           uint64_t sum2 = 0;
 #pragma unroll
@@ -595,6 +596,7 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1) paged_many_kernel(cons
     const uint32_t stage = sbase + C::Q0 + (warp >> 2) * C::TILE + ((tid & 127) >> 3) * 1024 + (tid & 7) * 128;
 #pragma unroll 1
     for (int c = 0; ok && c < D; c += 32) {
+      __syncwarp();
       float v[32];
       if (T > 0) {
         tmem_ld32(lane_tm + c, v);
@@ -622,8 +624,8 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1) paged_many_kernel(cons
           tc::sts128(stage + (chunk >> 3) * (128 * 128) + (((chunk & 7) ^ (tid & 7)) << 4), w[0], w[1], w[2], w[3]);
         }
       }
-      __syncwarp();
     }
+    __syncwarp();
     if (ok && !part) {
       constexpr int CPR = D / 8, RPI = 32 / CPR;
       const int c = lane % CPR;

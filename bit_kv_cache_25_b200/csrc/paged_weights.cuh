@@ -168,6 +168,7 @@ __global__ void __launch_bounds__(SumCfg<D>::THREADS, 2) paged_sums_kernel(const
 #pragma unroll 1
       for (int c0 = 0; c0 < 128; c0 += 32) {
         float x[32];
+        __syncwarp();  // (tensor memory wants the warp as one)
         tmem_ld32(lane_tm + (j & 1) * 128 + c0, x);
         float4 ls[8];
 #pragma unroll
