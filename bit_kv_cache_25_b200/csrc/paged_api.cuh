@@ -302,6 +302,8 @@ vq_status vq_paged_evict(const vq_paged_desc* desc, const vq_paged_cache* cache,
     return fail(VQ_ERR_INVALID_ARGUMENT, "keep %d must be >= 1 and hold sinks %d + recent %d", keep, sinks, recent);
   if ((int64_t(keep) + vq::kPage - 1) / vq::kPage > to_desc->max_pages)
     return fail(VQ_ERR_INVALID_ARGUMENT, "keep %d does not fit the %d pages of a row of to_table", keep, to_desc->max_pages);
+  if (lens < to_lens + batch && to_lens < lens + batch)  // heads of a sequence read its length at different times
+    return fail(VQ_ERR_INVALID_ARGUMENT, "to_lens overlaps lens");
   vq::PagedEvictParams p{};
   p.from = paged_pool(desc, cache, block_table);
   p.to = paged_pool(to_desc, to, to_table);

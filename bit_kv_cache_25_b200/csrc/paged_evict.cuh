@@ -166,7 +166,8 @@ __device__ __forceinline__ uint32_t e4m3_scaled(uint32_t pair, __half2 g) {
   return r;
 }
 
-// One CTA per (destination page, head, sequence): gathers its tokens' codes.
+// One CTA per (destination page, head, sequence): gathers its tokens' codes. Bound by memory (with the selection, 8 x 12
+// heads of 18720 tokens down to 9360: 130 us, 3.6 TB/s).
 template <int CODE, int D>
 __global__ void __launch_bounds__(128) paged_move_kernel(const __grid_constant__ PagedEvictParams p) {
   constexpr int LPR = D / 16, RPI = 128 / LPR;

@@ -344,7 +344,8 @@ vq_status vq_paged_weights(const vq_paged_desc* desc, const vq_paged_cache* cach
  * of the others, those of largest cache->weight (equal weights: the lowest slot; a
  * NaN counts as -inf). The kept tokens go in order to slots 0 .. of the sequence's
  * row of to_table in the pools `to` (pos and weight with them; without pos in
- * `cache` the slot is the position), and to_lens[b] = min(lens[b], keep). kept
+ * `cache` the slot is the position), and to_lens[b] = min(lens[b], keep), an array
+ * apart from lens. kept
  * [batch][kv_heads][keep] receives their source slots, -1 behind the last. A page's
  * new scale is the largest of its tokens' old ones; a code of another scale is
  * rounded once more. `to` may be the same pools, with pages that no sequence of

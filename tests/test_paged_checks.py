@@ -58,7 +58,7 @@ def _weights(d=None, c=None, q=None, lse=BAD, acc=1):
                                          ctypes.byref(q or _query()), lse, acc, None)
 
 
-def _evict(d=None, c=None, batch=2, table=BAD, lens=BAD, td=None, tc=None, to_table=BAD, to_lens=BAD, keep=64, sinks=0,
+def _evict(d=None, c=None, batch=2, table=BAD, lens=BAD, td=None, tc=None, to_table=BAD, to_lens=BAD + 64, keep=64, sinks=0,
            recent=0, kept=BAD):
     return vq.raw_lib().vq_paged_evict(ctypes.byref(d or _desc()), ctypes.byref(c or _cache()), batch, table, lens,
                                        ctypes.byref(td or _desc()), ctypes.byref(tc or _cache()), to_table, to_lens, keep,
@@ -113,7 +113,7 @@ def test_bad_attention_and_weights_outputs():
 
 def test_bad_evictions():
     for kw, st in [(dict(batch=0), INV), (dict(table=None), INV), (dict(lens=None), INV), (dict(to_table=None), INV),
-                   (dict(to_lens=BAD + 2), MIS), (dict(kept=None), INV), (dict(kept=BAD + 2), MIS), (dict(keep=0), INV),
+                   (dict(to_lens=BAD + 2), MIS), (dict(to_lens=BAD), INV), (dict(to_lens=BAD + 4), INV), (dict(kept=None), INV), (dict(kept=BAD + 2), MIS), (dict(keep=0), INV),
                    (dict(sinks=-1), INV), (dict(recent=-1), INV), (dict(sinks=40, recent=25), INV),
                    (dict(keep=4 * 64 + 1), INV), (dict(td=_desc(kv_heads=2)), INV), (dict(td=_desc(head_dim=128)), INV),
                    (dict(td=_desc(code=1)), INV), (dict(c=_cache(weight=None)), INV), (dict(tc=_cache(k=None)), INV),

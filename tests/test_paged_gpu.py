@@ -345,6 +345,13 @@ def test_padded_queries_of_any_content(n, G):
     p.attend(q, 0.125, q_lens=ql)
 
 
+@pytest.mark.parametrize("rows", [8, 9, 16, 17, 47, 48, 49, 128, 129, 256, 257])
+def test_rows_around_the_kernels_tiles(rows):
+    p = Paged(2, 1, 128, "int8", 7, seed=rows)
+    p.fill([rows + 100, 448])
+    p.attend(_q(p, 1, rows, torch.bfloat16), 0.09, causal=True)
+
+
 @pytest.mark.parametrize("n", [3, 140])
 def test_more_queries_than_tokens_leaves_rows_empty(n):
     p = Paged(2, 1, 64, "int8", 2, seed=n)
