@@ -380,11 +380,11 @@ struct FewCfg {
 // sequence). Every warp walks 32-token units of codes on its own. Its own asynchronous
 // copies bring the next unit's K as soon as this one's scores are taken, and the next V as
 // soon as this one's products are: one buffer each, so that 16 warps fit an SM. What limits
-// is the warps' own chain of loads, conversions and products (about 900 instructions a
-// unit, 0.6 issued a cycle and scheduler), so warps count for more than bytes in flight:
+// is the warps' own chain of loads, conversions and products (766 instructions a unit,
+// 0.53 issued a cycle and scheduler), so warps count for more than bytes in flight:
 // 32 ragged sequences of up to 10521 tokens, 8 key heads, took 126 us with three units in
-// flight and 8 warps an SM, 107 with one and 16, and 95 us (4.5 TB/s) with the scores
-// transposed.
+// flight and 8 warps an SM, 107 with one and 16, 96 with the scores transposed, and 90 us
+// (4.8 TB/s) with more splits.
 // K codes are read as the fragments of Q K^T, channels paired off between Q and K as one
 // wide load brings them; V codes by transposing 16-bit loads, which bring a thread two
 // channels of two tokens, the fragments of V^T P^T.

@@ -491,10 +491,13 @@ def _rows(name: str, t: torch.Tensor, heads: Optional[int], desc: PagedDesc):
     return shape
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # the handle without a Stream object around it
+
+
 def _handle(device: int, stream):
     """The stream a call runs on: the one given, or the device's current one."""
     if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream
+        return _raw_stream(device) if _raw_stream is not None else torch.cuda.current_stream(device).cuda_stream
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 

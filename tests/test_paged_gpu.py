@@ -395,6 +395,21 @@ def test_a_nan_or_infinite_query_stays_in_its_row():
         assert not torch.isfinite(out[0, 0, 1]).any() and not torch.isfinite(out[0, 1, 2]).any()
 
 
+@pytest.mark.parametrize("n,G,pages", [(1, 4, 400), (1, 16, 120), (3, 5, 90), (60, 1, 90), (3, 64, 70), (130, 2, 70)])
+@pytest.mark.parametrize("masks", ["plain", "all"])
+def test_a_long_axis_is_split_and_joined(n, G, pages, masks):
+    """One sequence and one head: its pages go to many CTAs, some of them with nothing to see."""
+    D = 64 if n == 3 else 128
+    p = Paged(1, 1, D, "e4m3" if G > 2 else "int8", pages, seed=pages + n, weight=pages < 400)
+    p.fill([pages * 64 - 29])
+    m = {}
+    if masks == "all":
+        first = p.g.integers(0, pages * 64, (1, n)).astype(np.int32)
+        first[0, 0] = pages * 64 - 100
+        m = dict(causal=True, softcap=20.0, slopes=2.0 ** -np.linspace(4, 12, G), prefix=[500], first=first)
+    p.attend(_q(p, G, n, torch.bfloat16, 2.0), D ** -0.5, **m)
+
+
 def test_repeats_to_the_bit_on_streams_and_with_a_workspace():
     p = Paged(3, 2, 128, "e4m3", 40, seed=4)
     p.fill([2500, 64, 1111])
