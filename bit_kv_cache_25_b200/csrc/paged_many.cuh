@@ -380,6 +380,9 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1) paged_many_kernel(cons
             if (move) R = t;
             l *= g;
             __syncwarp();
+            // what the first page stored (its weights; the output, if that page moved the reference too) is loaded again
+            // below: stores and loads of tensor memory have no order of their own
+            tc::tmem_wait_st();
             if (half) {  // the first page's weights of this tile
 #pragma unroll 1
               for (int c = 0; c < 32; c += 16) {
