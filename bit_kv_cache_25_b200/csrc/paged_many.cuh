@@ -14,14 +14,17 @@
 //   - one MMA warp: S = Q K^T, O += P V (P from tensor memory), ordered so that one
 //     tile's products run while the other's softmax does.
 // The scales stay out of the operands: K's is a factor of the scores, V's goes into the
-// weights as an exponent. A row's reference R covers z + log2(scale_V / v0), v0 the first
-// non-zero V scale of the item, and the row sum takes each page's part times v0 / scale_V
-// again, so weights keep their 11 bits whatever the pages' scales are (ratios to v0 are
-// cut at 2^+-100). R moves only when a row's maximum passes it by 8 (weights reach 2^15);
-// the output is then rescaled in tensor memory.
+// weights as an exponent, c = log2(scale_V / v0), v0 the first non-zero V scale of the item
+// (-inf for a page of zeros). A row has two references, so that both its output and its sum
+// keep their bits however far apart the pages' scales are: R covers z + c, the output's, and
+// L covers z, the sum's. A page's part of the sum is that of its weights, 2^(z + c - R + 7),
+// times 2^(R - c - L); a weight's exponent goes no lower than z - L - 53, where the weight is
+// zero in fp16 (at most 2^-45) and still counts in the sum. A reference moves only when a
+// row's maximum passes it by 8 (weights reach 2^15); the output is then rescaled in tensor
+// memory. (One reference and ratios cut at 2^+-100 took 935 us where two take 962, below.)
 //
-// 2 x 16 heads of 4096 queries over 10521 tokens: 930 us, 756 TFLOP/s. A period of 256 rows
-// and 128 keys takes about 4900 cycles; its products take 2240 and its exponentials 2050.
+// 2 x 16 heads of 4096 queries over 10521 tokens: 962 us, 734 TFLOP/s. A period of 256 rows
+// and 128 keys takes about 5050 cycles; its products take 2240 and its exponentials 2050.
 // What sets it is each query tile's chain (scores, softmax, P V, the next scores: P lies
 // over S, for which tensor memory has no second place at head_dim 128). A unit of 128 rows
 // would unpack K and V twice as often.
@@ -36,6 +39,9 @@
 
 namespace vq {
 namespace {
+
+// A row's references before it has seen a score: below every score, and finite, so that no sum of them is a NaN.
+constexpr float kNoScore = -3e38f;
 
 template <int D>
 struct ManyCfg {
@@ -250,7 +256,7 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1) paged_many_kernel(cons
   }
 
   bool ok = true;
-  float R = -INFINITY, l = 0.0f;
+  float R = kNoScore, L = kNoScore, l = 0.0f;  // references of the output and of the sum, and the sum
   if (T == 0) {
     // nothing to see: the rows are written below
   } else if (warp < 8) {
@@ -332,6 +338,7 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1) paged_many_kernel(cons
         for (int half = 0; half < 2; ++half) {  // one page: its scores stay in registers
           const int c0 = half * 64;
           const float f = half ? f1 : f0, lc = hdr[2 + half];
+          const float lz = hdr[4 + half];
           float(&x)[64] = xs[half];
           tc::tmem_wait_ld();
           if (MODE == kCap || (MODE == kGeneral && p.cap > 0.0f)) {
@@ -373,12 +380,12 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1) paged_many_kernel(cons
 #pragma unroll
             for (int k = 0; k < 4; ++k) mx[k] = tc::max3(mx[k], x[i + 2 * k], x[i + 2 * k + 1]);
           const float m = tc::max3(tc::max3(mx[0], x[60], x[61]), tc::max3(mx[1], x[62], x[63]), fmaxf(mx[2], mx[3]));
-          const float t = MODE == kPlain ? fmaf(m, f, lc) : m + lc;
-          const bool move = t > R + 8.0f;
-          if (__any_sync(0xffffffffu, move)) {
+          const float tz = MODE == kPlain ? fmaf(m, f, lz) : m + lz, t = tz + lc;
+          const bool move = t > R + 8.0f, move_l = tz > L + 8.0f;
+          if (__any_sync(0xffffffffu, move || move_l)) {
             const float g = move ? tc::ex2(R - t) : 1.0f;
             if (move) R = t;
-            l *= g;
+            if (move_l) l *= tc::ex2(L - tz), L = tz;
             __syncwarp();
             // what the first page stored (its weights; the output, if that page moved the reference too) is loaded again
             // below: stores and loads of tensor memory have no order of their own
@@ -410,7 +417,9 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1) paged_many_kernel(cons
             }
           }
           __syncwarp();  // (tensor memory wants the warp as one)
-          const float off = lc - (R == -INFINITY ? 0.0f : R) + 7.0f;
+          // weights are 2^(z + up + 7); no lower than z - L - 53, where they are zero in fp16 and still count in the sum
+          const float up = fmaxf(lc - R, (lz - 60.0f) - L), off = up + 7.0f;
+          const float from = tc::ex2(fminf(-up - L, 60.0f));  // from the weights' sum to the row's
           uint64_t sum2 = 0;
 #pragma unroll
           for (int ch = 0; ch < 64; ch += 32) {
@@ -428,7 +437,7 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1) paged_many_kernel(cons
             tc::tmem_st16(lane_tm + half * 32 + ch / 2, w);
             if (half == 0) tmem_ld32(lane_tm + 64 + ch, xs[1] + ch);  // the next page's, while these are worked on
           }
-          l = fmaf(tc::f2lo(sum2) + tc::f2hi(sum2), hdr[4 + half], l);
+          l = fmaf(tc::f2lo(sum2) + tc::f2hi(sum2), from, l);
         }
         tc::tmem_wait_st();
         tc::fence_before_sync();
@@ -480,17 +489,14 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1) paged_many_kernel(cons
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           hdr[i] = ks[i] * code_unit<CODE>();
-          float lc = 0.0f, inv = 1.0f;
-          if (vs[i] < 0.0f) {
-            lc = -INFINITY;  // no such page: its keys have no weight
-          } else if (vs[i] > 0.0f) {
+          float lc = -INFINITY;  // of zeros, or no such page
+          if (vs[i] > 0.0f) {
             if (v0 == 0.0f) *v0_slot = v0 = vs[i];
-            const float c = fminf(fmaxf(__fdiv_rn(vs[i], v0), 7.888609052210118e-31f), 1.2676506002282294e30f);
-            lc = log2f(c);
-            inv = __fdiv_rn(1.0f, c);
+            const float c = __fdiv_rn(vs[i], v0);
+            lc = c > 1e-30f && c < 1e30f ? log2f(c) : log2f(vs[i]) - log2f(v0);
           }
           hdr[2 + i] = lc;
-          hdr[4 + i] = inv;
+          hdr[4 + i] = vs[i] < 0.0f ? -INFINITY : 0.0f;  // no such page: its keys have no weight
         }
       }
       if (with_pos) reinterpret_cast<int2*>(hdr + 8)[u] = make_int2(pos, __float_as_int(static_cast<float>(pos - sv.pos0)));
@@ -598,8 +604,9 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1) paged_many_kernel(cons
     const int row = row0 + tid;
     const int i = row / p.G, hq = h * p.G + row % p.G;
     const bool part = p.splits > 1;
-    const float v0 = *v0_slot * code_unit<CODE>();
-    const float inv = part ? v0 : (l == 0.0f ? 0.0f : __fdiv_rn(v0, l));
+    // from the output's reference to the sum's, in two halves: 2^(R - L) may be past float32 where v0 makes up for it
+    const float half = tc::ex2(0.5f * (R - L));
+    const float inv = part ? half : (l == 0.0f ? 0.0f : __fdiv_rn(half, l)), v0 = *v0_slot * code_unit<CODE>() * half;
     const int64_t pr = (static_cast<int64_t>(split) * p.B * p.c.H + bh) * (static_cast<int64_t>(p.row_tiles) * 256) + row;
     // through the query tile's place in shared memory (its last product is done), to be stored as whole rows
     const uint32_t stage = sbase + C::Q0 + (warp >> 2) * C::TILE + ((tid & 127) >> 3) * 1024 + (tid & 7) * 128;
@@ -615,7 +622,7 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1) paged_many_kernel(cons
         for (int x = 0; x < 32; ++x) v[x] = 0.0f;
       }
 #pragma unroll
-      for (int x = 0; x < 32; ++x) v[x] *= inv;
+      for (int x = 0; x < 32; ++x) v[x] = v[x] * inv * v0;
       if (part) {
         if (rv.live) {
 #pragma unroll
@@ -651,9 +658,9 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1) paged_many_kernel(cons
     }
     if (ok && rv.live) {
       if (part)
-        p.part_ml[pr] = make_float2(R, l);
+        p.part_ml[pr] = make_float2(L, l);
       else if (p.lse)
-        p.lse[(static_cast<int64_t>(b) * p.Hq + hq) * p.n + i] = l == 0.0f ? -INFINITY : (R - 7.0f + log2f(l)) * kLn2;
+        p.lse[(static_cast<int64_t>(b) * p.Hq + hq) * p.n + i] = l == 0.0f ? -INFINITY : (L - 7.0f + log2f(l)) * kLn2;
     }
     tc::fence_before_sync();
   }

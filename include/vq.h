@@ -327,7 +327,8 @@ vq_status vq_paged_attention_workspace(const vq_paged_desc* desc, int32_t batch,
 
 /* out[b][hq][i] = sum_j e^(z_j - lse) v_j over the tokens seen, lse = ln sum e^z_j
  * ([batch][q_heads][n] float32, contiguous; may be NULL). A query that sees nothing
- * gets 0 and -inf. */
+ * gets 0 and -inf. V's scales may lie as far apart as they like; its largest magnitude
+ * times the tokens that a query sees has to stay below 2^112 (sums are float32). */
 vq_status vq_paged_attention(const vq_paged_desc* desc, const vq_paged_cache* cache, const vq_paged_query* query,
                              void* out, const int64_t out_strides[3], float* lse, void* workspace,
                              size_t workspace_bytes, void* stream);

@@ -18,9 +18,9 @@ def _rising(D, fmt, pages, step, n, dtype, G=1):
     for j in range(pages):
         page = p.table[0, j]
         c = p.g.integers(-3, 4, (64, D)).astype(np.float64)
-        c[:, 0] = 96.0
+        c[:, 0] = np.copysign(96.0, step)  # (a scale is never negative)
         p.o["k"][page, 0] = po.encode(c, fmt)
-        p.o["k_scale"][page, 0] = step / 96.0 * (j + 1)
+        p.o["k_scale"][page, 0] = abs(step) / 96.0 * (j + 1)
     p.push()
     q = _q(p, G, n, dtype, 0.02)
     q[..., 0] = 1.0
@@ -36,3 +36,66 @@ def test_a_reference_that_moves_in_every_page(n, G, pages, D, fmt, dtype):
     row's reference, and what the first of them stored is rescaled by the second."""
     p, q = _rising(D, fmt, pages, 6.5, n, dtype, G)
     p.attend(q, 1.0)
+
+
+@pytest.mark.parametrize("scales", ["tiny_first", "huge_first", "zeros", "mixed"])
+@pytest.mark.parametrize("n,dtype,D", [(1, torch.bfloat16, 128), (20, torch.float16, 64), (60, torch.bfloat16, 64),
+                                       (150, torch.bfloat16, 128), (150, torch.float16, 64), (300, torch.bfloat16, 128)])
+def test_v_scales_that_lie_far_apart(n, dtype, D, scales):
+    """Pages whose V differ by up to 2^215 and pages of zeros, in one sequence, seen together (whole rows) and apart
+    (causal rows and windows that see one kind of page only), with scores that favour either kind."""
+    p = Paged(2, 1, D, "int8", 6, seed=n)
+    p.fill([384, max(n, 200)])
+    power = {"tiny_first": [-120, -118, 0, 2, -3, 1], "huge_first": [90, 88, -5, 3, -100, 0],
+             "zeros": [None, None, -3, None, 4, None], "mixed": [0, -60, None, -119, 95, 20]}[scales]
+    if dtype == torch.float16:  # (whose outputs end at 65504: the largest scale is an ordinary one)
+        power = [e if e is None else e - max(x for x in power if x is not None) for e in power]
+        power = [e if e is None else max(e, -119) for e in power]
+    for b in range(2):
+        for j, e in enumerate(power):
+            page = p.table[b, j]
+            if e is None:
+                p.o["v"][page], p.o["v_scale"][page] = 0, 0.0
+            else:
+                p.o["v_scale"][page] *= 2.0 ** e
+    p.push()
+    q = _q(p, 2, n, dtype)
+    for scale in (0.05, 0.6):
+        p.attend(q, scale, causal=True)
+        p.attend(q, scale)
+    first = np.minimum(p.g.integers(0, 384, (2, n)), (p.lens - n)[:, None] + np.arange(n)[None]).astype(np.int32)
+    p.attend(q, 0.3, causal=True, first=first)
+
+
+@pytest.mark.parametrize("n", [1, 150])
+def test_the_largest_and_smallest_v(n):
+    """V as large as vq.h allows (times the tokens seen 2^112), and down to scales of 2^-126."""
+    for e in (103, -119):
+        p = Paged(1, 1, 64, "int8", 4, seed=n)
+        p.fill([200])
+        x = p.g.normal(size=p.o["v_scale"].shape)
+        p.o["v_scale"][...] = np.maximum(np.exp(0.3 * x) * 2.0 ** (e - 7), 2.0 ** -126)
+        p.push()
+        p.attend(_q(p, 4, n, torch.bfloat16), 0.3, causal=n > 1)
+
+
+@pytest.mark.parametrize("n", [1, 20, 150])
+def test_a_bad_page_among_very_low_scores(n):
+    """Tokens of a page id out of range count as unseen, also where every score that is seen lies far below 0."""
+    p, q = _rising(64, "int8", 4, -150.0, n, torch.bfloat16)
+    for bad in (0, 1, 3):
+        table = p.dtable.clone()
+        table[0, bad] = -1
+        out, lse = torch.zeros_like(q), torch.zeros(q.shape[:3], device="cuda")
+        vq.vq_paged_attention(p.desc, p.cache, table, p.dev(p.lens), q, 1.0, out, lse)
+        torch.cuda.synchronize()
+        assert vq.vq_poll_device_error() == 4
+        k, v = (x.astype(np.float64) for x in po.read(p.o, p.table, 0, 0, 0, int(p.lens[0])))
+        keep = [j for j in range(int(p.lens[0])) if j // 64 != bad]
+        z = q[0, 0].double().cpu().numpy() @ k[keep].T
+        want, wlse, w = po.attention(z, v[keep])
+        # the score's float32 error at this size (products of 64 channels, z to log2 units and back), weights to fp16
+        dz = np.abs(z).max() * (64 + 16 + 8) * 2.0 ** -24
+        tol = 2.0 ** -8 * np.abs(want) + (2.0 ** -11 + 2 * dz + 2.0 ** -19) * (w @ np.abs(v[keep])) + 1e-6
+        assert (np.abs(out[0, 0].double().cpu().numpy() - want) <= tol).all(), bad
+        assert (np.abs(lse[0, 0].double().cpu().numpy() - wlse) <= 2 * dz + np.abs(wlse) * 2.0 ** -22 + 1e-4).all(), bad
