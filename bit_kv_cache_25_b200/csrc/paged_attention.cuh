@@ -66,20 +66,23 @@ __device__ __forceinline__ void mma_16816_from_zero(float (&d)[4], const uint32_
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
-// cap * tanh(z / cap), times log2 e. tanh(x) = 1 - 2 / (e^2x + 1): its error is a few
-// 2^-24 of the cap, and it saturates without a NaN at both ends.
-__device__ __forceinline__ float capped(float z, float cap, float two_log2e_over_cap) {
-  const float e = tc::ex2(z * two_log2e_over_cap);
-  return (cap - __fdividef(2.0f * cap, e + 1.0f)) * kLog2e;
-}
-// The same of z = a * f where |z| <= cap / 4: tanh(x) = x * P(x^2), P of degree 2 interpolated at the Chebyshev nodes
-// of [0, 1/16] (4.2e-07 of itself off at most). Two multiply-adds in place of two more turns of the exponential unit, which
-// most scores are small enough for: a warp decides for all of its values.
+// cap * tanh(z / cap), times log2 e, of z = a * f: its error is a few 2^-24 of the smaller of |z| and the cap, so that a
+// large cap is close to none. Two forms:
+// |z| <= cap / 4: tanh(x) = x * P(x^2), P of degree 2 interpolated at the Chebyshev nodes of [0, 1/16] (4.2e-07 of itself
+// off at most). Most scores are small enough for it, and it takes two multiply-adds where the other takes two turns of the
+// exponential unit: a warp decides for all of its values.
 constexpr float kCapSmall = 0.25f;
 __device__ __forceinline__ float capped_small(float a, float f_over_cap, float cap_log2e) {
   const float x = a * f_over_cap, y = x * x;
   const float t = fmaf(fmaf(0.1284143328666687f * cap_log2e, y, -0.3332189619541168f * cap_log2e), y, 0.9999995827674866f * cap_log2e);
   return x * t;
+}
+// Any z, where a warp has larger ones: beyond cap / 4 tanh(x) = 1 - 2 / (e^2x + 1), which saturates without a NaN at both
+// ends (and cancels below: its error is a few 2^-24 of the cap).
+__device__ __forceinline__ float capped(float z, float cap, float over_cap, float two_log2e_over_cap) {
+  const float e = tc::ex2(z * two_log2e_over_cap);
+  const float large = (cap - __fdividef(2.0f * cap, e + 1.0f)) * kLog2e;
+  return fabsf(z) <= kCapSmall * cap ? capped_small(z, over_cap, cap * kLog2e) : large;
 }
 
 // What a row sees: slots [0, hi), or positions below `prefix` up to slot `len`, from position `first` on.
@@ -316,6 +319,37 @@ __device__ __forceinline__ void finish_scores(const PagedAttnParams& p, const Se
 #pragma unroll
     for (int e = 0; e < 2; ++e) fr[half][e] = f * back[half][e];
 #pragma unroll
+  for (int x = 0; x < 4; ++x)
+#pragma unroll
+    for (int half = 0; half < ROWS / 8; ++half)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) s[x >> 1][half][2 * (x & 1) + e] *= fr[half][e];
+  if (cap) {
+    float top = 0.0f;
+#pragma unroll
+    for (int half = 0; half < ROWS / 8; ++half)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) top = fmaxf(top, fmaxf(fabsf(s[0][half][i]), fabsf(s[1][half][i])));
+    const float over = 0.5f * kLn2 * cap_f, cl = p.cap * kLog2e;  // (over: 1 / cap)
+    if (__all_sync(0xffffffffu, top <= kCapSmall * p.cap)) {
+#pragma unroll
+      for (int half = 0; half < ROWS / 8; ++half)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          s[0][half][i] = capped_small(s[0][half][i], over, cl);
+          s[1][half][i] = capped_small(s[1][half][i], over, cl);
+        }
+    } else {
+#pragma unroll
+      for (int half = 0; half < ROWS / 8; ++half)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          s[0][half][i] = capped(s[0][half][i], p.cap, over, cap_f);
+          s[1][half][i] = capped(s[1][half][i], p.cap, over, cap_f);
+        }
+    }
+  }
+#pragma unroll
   for (int x = 0; x < 4; ++x) {
     const int key = 8 * x + (lane >> 2), slot = slot0 + key;
     int kp = slot;
@@ -330,17 +364,12 @@ __device__ __forceinline__ void finish_scores(const PagedAttnParams& p, const Se
       for (int e = 0; e < 2; ++e) {
         const RowView& rv = rows.v[half][e];
         float z = s[x >> 1][half][2 * (x & 1) + e];
-        if (MODE == kPlain) {
-          z *= fr[half][e];
-        } else {
-          z *= fr[half][e];
-          z = cap ? capped(z, p.cap, cap_f) : z * kLog2e;
-          if (MODE == kGeneral) {
-            z = fmaf(-rv.slope, fabsf(rv.pos - kf), z);
-            if (by_pos) {
-              const bool see = slot < sv.len && (slot < rv.hi || (kp < prefix && rv.hi >= 0)) && kp >= rv.first;
-              z = see ? z : -INFINITY;
-            }
+        if (MODE == kGeneral) {
+          if (!cap) z *= kLog2e;
+          z = fmaf(-rv.slope, fabsf(rv.pos - kf), z);
+          if (by_pos) {
+            const bool see = slot < sv.len && (slot < rv.hi || (kp < prefix && rv.hi >= 0)) && kp >= rv.first;
+            z = see ? z : -INFINITY;
           }
         }
         if (masked && (slot < rows.lo[half][e] || slot >= rows.hi[half][e])) z = -INFINITY;

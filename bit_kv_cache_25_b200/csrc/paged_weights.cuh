@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(SumCfg<D>::THREADS, 2) paged_sums_kernel(const
             for (int i = 0; i < 32; ++i) x[i] = capped_small(x[i], fc, cl);
           } else if (cap) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] = capped(x[i] * f, p.cap, cap_f);
+            for (int i = 0; i < 32; ++i) x[i] = capped(x[i] * f, p.cap, over, cap_f);
           } else {
 #pragma unroll
             for (int i = 0; i < 32; ++i) x[i] *= f * kLog2e;

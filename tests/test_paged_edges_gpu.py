@@ -99,3 +99,35 @@ def test_a_bad_page_among_very_low_scores(n):
         tol = 2.0 ** -8 * np.abs(want) + (2.0 ** -11 + 2 * dz + 2.0 ** -19) * (w @ np.abs(v[keep])) + 1e-6
         assert (np.abs(out[0, 0].double().cpu().numpy() - want) <= tol).all(), bad
         assert (np.abs(lse[0, 0].double().cpu().numpy() - wlse) <= 2 * dz + np.abs(wlse) * 2.0 ** -22 + 1e-4).all(), bad
+
+
+@pytest.mark.parametrize("cap", [1.0, 50.0, 1e3, 1e4, 1e6])
+@pytest.mark.parametrize("n,G,pos", [(1, 4, False), (9, 2, True), (60, 1, False), (130, 2, True)])
+def test_a_cap_of_any_size_is_exact_for_scores_far_below_it(cap, n, G, pos, monkeypatch):
+    """Scores of a few units under caps up to 1e6: close to no cap. One key far below the others (beyond a quarter of
+    the cap) must not cost the others their bits."""
+    scores = po.scores
+
+    def without_the_far_ones(*a, **kw):
+        z, err = scores(*a, **kw)  # (a key 200 below the row's best has no weight, whatever its score's error)
+        return z, np.where(z < z.max(1, keepdims=True) - 200.0, 0.0, err)
+
+    monkeypatch.setattr(po, "scores", without_the_far_ones)
+    for low in (False, True):
+        p = Paged(1, 2, 64, "int8", 5, seed=n)
+        p.fill([300])
+        if low:
+            page = p.table[0, 1]
+            for name in ("k", "v"):
+                p.o[name][page] = po.encode(p.g.integers(-2, 3, p.o[name][page].shape).astype(np.float64), "int8")
+            p.o["k"][page, :, 5, 0] = po.encode(np.array(-127.0), "int8")
+            p.o["k_scale"][page] = np.float32(cap / 127)  # channel 0 of that key: -cap, of the other keys +-2 / 127 cap
+            p.o["k"][page, :, :5, 0] = 0
+            p.o["k"][page, :, 6:, 0] = 0
+        p.push()
+        q = _q(p, 2 * G, n, torch.bfloat16, 0.5)
+        if low:
+            q[..., 0] = 1.0
+            q[..., 1:] *= min(1.0, 100.0 / cap)
+        m = dict(slopes=2.0 ** -np.arange(1, 2 * G + 1), causal=True, prefix=[70]) if pos else {}
+        p.attend(q, 0.4, softcap=cap, **m)

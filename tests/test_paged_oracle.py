@@ -129,3 +129,13 @@ def test_planted_mistakes_are_seen(mistake, monkeypatch):
         monkeypatch.setattr(po, "keep_slots", lambda w, n, keep, s, r: real_keep(w, n, keep, s, 0))
         with pytest.raises(AssertionError):
             test_eviction_order()
+
+
+def test_a_large_cap_is_close_to_none():
+    c = _cache(1, 1, 64, "int8", pos=False)
+    x = np.random.default_rng(4).normal(size=(1, 1, 60, 64)).astype(np.float32)
+    po.append(c, [[0]], [0], [60], x, x)
+    q = np.random.default_rng(5).normal(size=(2, 64))
+    z0, e0 = po.scores(c, [[0]], 0, 0, 0, 60, q, 0.125, q_len=2)
+    z1, e1 = po.scores(c, [[0]], 0, 0, 0, 60, q, 0.125, q_len=2, cap=1e6)
+    assert np.abs(z1 - z0).max() <= 1e-9 and (e1 - e0 <= np.abs(z0) * 2.0 ** -18).all()
