@@ -774,8 +774,10 @@ __global__ void __launch_bounds__(kFewWarps * 32) paged_weights_kernel(const __g
 #pragma unroll
         for (int half = 0; half < NH; ++half)
 #pragma unroll
-          for (int e = 0; e < 2; ++e)
-            w += base[half][e] == INFINITY ? 0.0f : tc::ex2(s[x >> 1][half][2 * (x & 1) + e] - base[half][e]);
+          for (int e = 0; e < 2; ++e) {
+            const float z = s[x >> 1][half][2 * (x & 1) + e];  // (an unseen key has no weight whatever the row's lse, NaN included)
+            w += base[half][e] == INFINITY || z == -INFINITY ? 0.0f : tc::ex2(z - base[half][e]);
+          }
         w += __shfl_xor_sync(0xffffffffu, w, 1);
         w += __shfl_xor_sync(0xffffffffu, w, 2);
         if (x == c) mine = w;

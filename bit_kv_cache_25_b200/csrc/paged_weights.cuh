@@ -243,8 +243,8 @@ __global__ void __launch_bounds__(SumCfg<D>::THREADS, 2) paged_sums_kernel(const
       lse = -INFINITY;
       if (v.hi >= 0) {
         const int i = row / p.G, hq = h * p.G + row % p.G;
-        at = b * p.q_sb + hq * p.q_sh + i * p.q_st;
         lse = __ldg(p.lse + (static_cast<int64_t>(b) * p.Hq + hq) * p.n + i);
+        if (lse != -INFINITY) at = b * p.q_sb + hq * p.q_sh + i * p.q_st;  // (a row that saw nothing: zeros, whatever its bytes)
       }
     };
     if (T > 0) look(0);

@@ -131,3 +131,40 @@ def test_a_cap_of_any_size_is_exact_for_scores_far_below_it(cap, n, G, pos, monk
             q[..., 1:] *= min(1.0, 100.0 / cap)
         m = dict(slopes=2.0 ** -np.arange(1, 2 * G + 1), causal=True, prefix=[70]) if pos else {}
         p.attend(q, 0.4, softcap=cap, **m)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("n", [4, 20, 150])
+def test_weights_of_queries_of_any_content(n, causal):
+    """A live query of NaN or infinity that sees nothing gives no weight to anything; one that sees some tokens spoils
+    those and leaves what it does not see alone."""
+    L = 250 if causal else 640  # (causal or not: tiles of keys that only some rows see, or all but those that see nothing)
+    p = Paged(1, 2, 64, "int8", 10, seed=n, pos=False)
+    p.fill([L])
+    q = _q(p, 4, n, torch.bfloat16)
+    first = np.zeros((1, n), np.int32)
+    first[0, 1] = 2 ** 30          # sees nothing
+    first[0, 2] = L - n            # sees the call's own tokens, its first three where causal
+    args = dict(first=p.dev(first), causal=causal)
+
+    def weights(q):
+        out, lse = torch.zeros_like(q), torch.zeros((1, 4, n), device="cuda")
+        vq.vq_paged_attention(p.desc, p.cache, p.dtable, p.dev(p.lens), q, 0.125, out, lse, **args)
+        vq.vq_paged_weights(p.desc, p.cache, p.dtable, p.dev(p.lens), q, 0.125, lse, accumulate=False, **args)
+        torch.cuda.synchronize()
+        assert vq.vq_poll_device_error() == 0
+        return np.array([po.per_slot({"weight": p.cache.weight.cpu().numpy()}, "weight", p.table, 0, h, L) for h in range(2)]), lse
+
+    good, lse = weights(q)
+    assert torch.isneginf(lse[0, :, 1]).all() and np.isfinite(good).all()
+    for bad in (float("nan"), float("inf"), float("-inf")):
+        x = q.clone()
+        x[0, :, 1] = bad
+        got, _ = weights(x)
+        assert np.array_equal(got, good), bad
+        x[0, :2, 2] = bad          # key head 0's queries
+        got, lse = weights(x)
+        assert torch.isnan(lse[0, :2, 2]).all() and np.array_equal(got[1], good[1])
+        hit = np.zeros(L, bool)
+        hit[L - n:L - n + 3 if causal else L] = True
+        assert np.isnan(got[0][hit]).all() and np.array_equal(got[0][~hit], good[0][~hit]), bad
