@@ -173,7 +173,8 @@ __global__ void __launch_bounds__(128) paged_move_kernel(const __grid_constant__
   constexpr int LPR = D / 16, RPI = 128 / LPR;
   __shared__ int64_t sm_src[kPage];  // (page * H + head) * 64 + slot, -1: none
   __shared__ float sm_scale[2][kPage];
-  __shared__ double sm_ratio[2][kPage];  // old scale over the page's new one
+  __shared__ float sm_ratio[2][kPage];  // old scale over the page's new one
+  __shared__ float sm_top[2];            // the new one
   const int per = (p.keep + kPage - 1) / kPage;
   const int tile = blockIdx.x % per, bh = blockIdx.x / per;
   const int b = bh / p.from.H, h = bh - b * p.from.H;
@@ -208,9 +209,9 @@ __global__ void __launch_bounds__(128) paged_move_kernel(const __grid_constant__
     float top = fmaxf(sm_scale[t][tid & 31], sm_scale[t][32 + (tid & 31)]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if ((tid & 63) == 0) p.to.scale[t][dst] = top;
+    if ((tid & 63) == 0) p.to.scale[t][dst] = sm_top[t] = top;
     const float s = sm_scale[t][tid & 63];
-    sm_ratio[t][tid & 63] = s == top ? 1.0 : static_cast<double>(s) / static_cast<double>(top);
+    sm_ratio[t][tid & 63] = s == top ? 1.0f : __fdiv_rn(s, top);
   }
   __syncthreads();
 #pragma unroll
@@ -226,25 +227,38 @@ __global__ void __launch_bounds__(128) paged_move_kernel(const __grid_constant__
     for (int i = 0; i < kPage / RPI; ++i) {
       const int slot = i * RPI + tid / LPR;
       if (slot >= held) continue;
-      const double f = sm_ratio[t][slot];
-      if (f != 1.0) {
+      const float ratio = sm_ratio[t][slot];
+      if (sm_scale[t][slot] != sm_top[t]) {
         if (CODE == kCodeInt8) {
-          // the quotient of an 8-bit and two 24-bit numbers is at least 2^-33 from any half that it
-          // does not equal: in 64 bits it rounds as the real number does
+          // the quotient code * old / new in float32 is off by less than 127 * 2^-22; next to a half it is taken in 64
+          // bits, where code * old is exact and the quotient either a half exactly or at least 2^-33 from one: it
+          // rounds as the real number does (a ratio rounded first would miss the halves)
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
             const uint32_t o = (&v[i].x)[w];
             uint32_t r = 0;
+            bool near = false;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              const int k = __double2int_rn(static_cast<double>(code_value<CODE>((o >> (8 * j)) & 0xff)) * f);
+              const float q = code_value<CODE>((o >> (8 * j)) & 0xff) * ratio;
+              const int k = __float2int_rn(q);
+              near |= fabsf(q - static_cast<float>(k)) > 0.4999f;
               r |= (static_cast<uint32_t>(k) & 0xff) << (8 * j);
+            }
+            if (near) {
+              const double from = sm_scale[t][slot], to = sm_top[t];
+              r = 0;
+#pragma unroll 1
+              for (int j = 0; j < 4; ++j) {
+                const int k = __double2int_rn(static_cast<double>(code_value<CODE>((o >> (8 * j)) & 0xff)) * from / to);
+                r |= (static_cast<uint32_t>(k) & 0xff) << (8 * j);
+              }
             }
             (&v[i].x)[w] = r;
           }
         } else {
           // a power of two (2^-24 and less leave nothing of any code): exact in fp16 wherever the result is not 0
-          const __half2 g = __half2half2(__float2half_rn(static_cast<float>(f)));
+          const __half2 g = __half2half2(__float2half_rn(ratio));
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
             const uint32_t o = (&v[i].x)[w];

@@ -133,6 +133,30 @@ def test_a_cap_of_any_size_is_exact_for_scores_far_below_it(cap, n, G, pos, monk
         p.attend(q, 0.4, softcap=cap, **m)
 
 
+def test_evicted_codes_whose_quotient_is_a_tie():
+    """Tokens of pages of scale 15 join a page of scale 22 (times a power of two): 11 * 15 / 22 = 7.5 exactly, and so on:
+    to the even code."""
+    for num, den in ((15, 22), (5, 26), (7, 38), (21, 22), (125, 254), (3, 2 ** 20 + 2)):
+        p = Paged(1, 1, 64, "int8", 2, seed=num)
+        p.lens = np.array([128], np.int32)
+        p.o["k"][...] = p.o["v"][...] = 0
+        codes = np.concatenate([np.arange(-127, 128), [0]]).astype(np.int8).view(np.uint8).reshape(4, 64)
+        for n in ("k", "v"):
+            p.o[n][p.table[0, 0], 0, :4] = codes
+            p.o[n + "_scale"][...] = np.float32(num * 2.0 ** -9)
+            p.o[n + "_scale"][p.table[0, 1]] = np.float32(den * 2.0 ** -9)
+        p.o["weight"][...] = 0
+        p.o["weight"][p.table[0, 0], 0, :4] = 1
+        p.o["weight"][p.table[0, 1], 0, 7] = 1
+        p.push()
+        to = Paged(1, 1, 64, "int8", 1, seed=1)
+        kept, to_lens = torch.zeros((1, 1, 5), dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+        vq.vq_paged_evict(p.desc, p.cache, p.dtable, p.dev(p.lens), to.desc, to.cache, to.dtable, to_lens, 5, kept=kept)
+        po.evict(p.o, p.table, p.lens, to.o, to.table, 5, 0, 0)
+        assert kept.tolist() == [[[0, 1, 2, 3, 71]]]
+        to.check()
+
+
 @pytest.mark.parametrize("causal", [True, False])
 @pytest.mark.parametrize("n", [4, 20, 150])
 def test_weights_of_queries_of_any_content(n, causal):
