@@ -351,14 +351,15 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const __gr
         for (int j = 0; j < 4; ++j) {
           tt[j] = __fmaf_rn(xv[j], inv, 12582912.0f);
           k[j] = tt[j] - 12582912.0f;
-          off |= fabsf(__fmaf_rn(-k[j], scale, xv[j])) >= half;
+          off |= fabsf(__fmaf_rn(-k[j], scale, xv[j])) >= half;  // (remainders are multiples of 2^-149: none lies between half and its float)
         }
         if (off) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const float rem = __fmaf_rn(-k[j], scale, xv[j]);
             const bool odd = (__float_as_uint(tt[j]) & 1u) != 0;
-            if (fabsf(rem) > half || (fabsf(rem) == half && odd)) tt[j] += rem > 0.0f ? 1.0f : -1.0f;
+            // (twice the remainder: half of a scale below 2^-125 may be no float)
+            if (fabsf(rem + rem) > scale || (fabsf(rem + rem) == scale && odd)) tt[j] += rem > 0.0f ? 1.0f : -1.0f;
           }
         }
         uint32_t a = __byte_perm(__float_as_uint(tt[0]), __float_as_uint(tt[1]), 0x0040);

@@ -192,3 +192,18 @@ def test_weights_of_queries_of_any_content(n, causal):
         hit = np.zeros(L, bool)
         hit[L - n:L - n + 3 if causal else L] = True
         assert np.isnan(got[0][hit]).all() and np.array_equal(got[0][~hit], good[0][~hit]), bad
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_append_of_scales_whose_half_is_not_a_float(dtype):
+    """Scales just above 2^-126 with an odd last bit: quotients next to a half go to their nearest code."""
+    p = Paged(1, 1, 64, "int8", 8, seed=3)
+    for j in range(8):
+        s = 2.0 ** -126 + (2 * j + 1) * 2.0 ** -149
+        x = np.float64(np.arange(-64, 64)[:, None] * s)
+        x = np.rint((x + 0.5 * s) / 2.0 ** -149) + p.g.integers(-1, 2, x.shape)
+        x = np.concatenate([x.reshape(2, 64) * 2.0 ** -149, np.zeros((62, 64))]).astype(np.float32)
+        x[2, 0] = np.float32(127 * s)
+        t = torch.from_numpy(x)[None, None].cuda().to(dtype)
+        p.append(t, t)
+    p.check()
