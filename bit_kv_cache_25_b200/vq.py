@@ -610,7 +610,8 @@ def vq_paged_weights(desc: PagedDesc, cache: PagedCache, block_table: torch.Tens
                      first=None, slopes=None, softcap: float = 0.0, causal: bool = False, accumulate: bool = True,
                      stream=None):
     """Per cached token the sum of its attention weights over these queries (and the query heads
-    of its key head), added to cache.weight or put there; lse as vq_paged_attention gave it."""
+    of its key head), added to cache.weight or put there; lse as vq_paged_attention gave it.
+    No two sequences of a call may share a page: call it for them one after the other."""
     dev = _paged_cache_check(desc, cache)
     if cache.weight is None:
         raise ValueError("the cache has no weight")

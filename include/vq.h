@@ -243,8 +243,13 @@ vq_status vq_dequantize(const vq_cache_desc* desc, int32_t block, const uint32_t
  *   - What lies in a page behind its sequence's last token is never used, whatever
  *     its bytes. Rows of padded queries (i >= q_lens[b]) are neither read nor
  *     written.
- *   - Two sequences of one append must not share a page that it writes; shared
- *     pages may be read by any number.
+ *   - Sequences may share pages (a common prefix): append, attention, read and
+ *     eviction read a page for any number of them. A call must not write one page
+ *     for two: two sequences of one append share no page that it writes, and two
+ *     sequences of one vq_paged_weights call share no page at all, since the
+ *     weight of a page's tokens is one number (nothing checks it: their sums would
+ *     lose parts). Call it for sequences that share pages one after the other,
+ *     accumulating; their pages then hold the sum over all of them.
  *   - Results do not depend on the order in which blocks run: the same call on the
  *     same inputs repeats to the bit.
  *   - Supported: head_dim 64 or 128; any kv_heads; queries and outputs in bf16 or
@@ -336,7 +341,8 @@ vq_status vq_paged_attention(const vq_paged_desc* desc, const vq_paged_cache* ca
 /* Per cached token and key head the sum of the weights e^(z_j - lse) over the
  * call's queries and the query heads of that key head, with lse as
  * vq_paged_attention gave it for the same query: added to cache->weight
- * (accumulate 1) or put there (0), for tokens j < lens[b]. */
+ * (accumulate 1) or put there (0), for tokens j < lens[b]. No two sequences of a
+ * call share a page. */
 vq_status vq_paged_weights(const vq_paged_desc* desc, const vq_paged_cache* cache, const vq_paged_query* query,
                            const float* lse, int32_t accumulate, void* stream);
 

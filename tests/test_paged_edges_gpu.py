@@ -207,3 +207,54 @@ def test_append_of_scales_whose_half_is_not_a_float(dtype):
         t = torch.from_numpy(x)[None, None].cuda().to(dtype)
         p.append(t, t)
     p.check()
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+def test_sequences_that_share_pages(fmt):
+    """A common prefix of two pages, one of them with other pages behind it: read, attended and evicted from by all;
+    weights by one call after the other, which sum up."""
+    p = Paged(3, 2, 64, fmt, 6, seed=21, pos=False, weight=False)
+    p.table[1, :2] = p.table[2, :2] = p.table[0, :2]
+    p.dtable = p.dev(p.table)
+    p.fill([300, 200, 131])
+    x = [torch.zeros((3, 2, 128, 64), device="cuda") for _ in range(2)]
+    vq.vq_paged_read(p.desc, p.cache, p.dtable, p.dev(np.zeros(3, np.int32)), *x)
+    for b in range(3):
+        for h in range(2):
+            assert np.array_equal(x[0][b, h].cpu().numpy(), po.read(p.o, p.table, 0, h, 0, 128)[0])
+    for n in (1, 20, 60, 150):
+        p.attend(_q(p, 4, n, torch.bfloat16), 0.125, causal=True)
+    # what each appends behind the prefix is its own
+    p.append(*p.tokens(40))
+    p.check()
+    p.attend(_q(p, 4, 3, torch.bfloat16), 0.125, causal=True)
+
+    cache = vq.PagedCache(p.desc, k=p.cache.k, v=p.cache.v, k_scale=p.cache.k_scale, v_scale=p.cache.v_scale,
+                          weight=torch.zeros(p.cache.k.shape[:3], device="cuda"))
+    for n in (2, 60):
+        q = _q(p, 4, n, torch.bfloat16)
+        lens, out, lse = p.dev(p.lens), torch.zeros_like(q), torch.zeros((3, 4, n), device="cuda")
+        vq.vq_paged_attention(p.desc, p.cache, p.dtable, lens, q, 0.125, out, lse, causal=True)
+        cache.weight.zero_()
+        for b in range(3):
+            i = slice(b, b + 1)
+            vq.vq_paged_weights(p.desc, cache, p.dtable[i], lens[i], q[i], 0.125, lse[i], causal=True)
+        got = cache.weight.cpu().numpy()
+        w, wt = p.expect(q, 0.125, np.full(3, n), causal=True)[4:]
+        want, tol = np.zeros(got.shape), np.zeros(got.shape)
+        for b in range(3):
+            for h in range(2):
+                for j in range(int(p.lens[b])):
+                    at = p.table[b, j // 64], h, j % 64
+                    want[at] += w[b][h][j]
+                    tol[at] += wt[b][h][j]
+        assert (np.abs(got - want) <= tol + np.abs(want) * 2.0 ** -22).all()
+    p.cache = cache
+    p.o["weight"] = got
+    keep = 100
+    to = Paged(3, 2, 64, fmt, 2, seed=22)
+    kept, to_lens = torch.zeros((3, 2, keep), dtype=torch.int32, device="cuda"), torch.zeros(3, dtype=torch.int32, device="cuda")
+    vq.vq_paged_evict(p.desc, p.cache, p.dtable, p.dev(p.lens), to.desc, to.cache, to.dtable, to_lens, keep, sinks=2, recent=7, kept=kept)
+    want, _ = po.evict(p.o, p.table, p.lens, to.o, to.table, keep, 2, 7)
+    assert np.array_equal(kept.cpu().numpy(), want)
+    to.check()
