@@ -306,7 +306,9 @@ vq_status vq_paged_read(const vq_paged_desc* desc, const vq_paged_cache* cache, 
  *   seen if  (not causal, or j <= lens[b] - q_lens[b] + i, or p_j < prefix[b])
  *        and (first NULL, or p_j >= first[b][i]).
  * `first` is the first token of the query's document in a sequence of several, or
- * the start of its window. After an eviction positions have gaps: pass q_pos. */
+ * the start of its window. It hides what lies before, no more: with causal it makes
+ * a document mask; without, a query also sees all that lies behind its document.
+ * After an eviction positions have gaps: pass q_pos. */
 typedef struct {
   int32_t batch, q_heads, n;
   vq_dtype dtype;             /* VQ_BF16 or VQ_F16, of q and out */

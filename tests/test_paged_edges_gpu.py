@@ -258,3 +258,12 @@ def test_sequences_that_share_pages(fmt):
     want, _ = po.evict(p.o, p.table, p.lens, to.o, to.table, keep, 2, 7)
     assert np.array_equal(kept.cpu().numpy(), want)
     to.check()
+
+
+@pytest.mark.parametrize("n,G,pos", [(1, 4, False), (20, 2, True), (60, 1, False), (150, 2, True), (150, 1, False)])
+def test_a_lower_bound_without_a_causal_mask_hides_nothing_behind(n, G, pos):
+    """`first` alone is a lower bound: what lies behind a query is seen to the sequence's end."""
+    p = Paged(2, 2, 64, "int8", 5, seed=n, pos=pos)
+    p.fill([320, max(n, 131)])
+    first = p.g.integers(0, 320, (2, n)).astype(np.int32)
+    p.attend(_q(p, 2 * G, n, torch.bfloat16, 2.0), 0.125, first=first)
