@@ -5,7 +5,7 @@
 // paged_attention.cuh) of one (sequence, key head) against its pages, 128 keys
 // (two pages) at a time. One CTA per item and SM:
 //   - two softmax warpgroups, one thread per row: query rows to shared memory
-//     (bf16 rows times a power of two, exact in fp16), then per key tile the row
+//     (bf16 rows times a power of two, as fp16), then per key tile the row
 //     maximum, 2^(z - R + 7) as fp16 over the scores' own columns, and at the end
 //     the output;
 //   - four warps unpack K and three V: codes straight from global memory into

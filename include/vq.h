@@ -322,7 +322,7 @@ typedef struct {
   const int32_t* first;       /* [batch][n] or NULL */
   const float* slopes;        /* [q_heads] or NULL */
   float softmax_scale;        /* (0, 1e6] */
-  float softcap;              /* 0 or (0, 1e6] */
+  float softcap;              /* 0 or [1e-6, 1e6] */
   int32_t causal;             /* 0 or 1 */
 } vq_paged_query;
 
@@ -335,7 +335,17 @@ vq_status vq_paged_attention_workspace(const vq_paged_desc* desc, int32_t batch,
 /* out[b][hq][i] = sum_j e^(z_j - lse) v_j over the tokens seen, lse = ln sum e^z_j
  * ([batch][q_heads][n] float32, contiguous; may be NULL). A query that sees nothing
  * gets 0 and -inf. V's scales may lie as far apart as they like; its largest magnitude
- * times the tokens that a query sees has to stay below 2^112 (sums are float32). */
+ * times the tokens that a query sees has to stay below 2^112 (sums are float32).
+ * Arithmetic: codes and fp16 queries are exact operands; a row of bf16 queries is
+ * taken to fp16 times a power of two, exactly down to 2^-24 of the row's largest
+ * magnitude and within 2^-32 of that magnitude below it. Products, sums, scales,
+ * caps (within 2^-21 of the score, or of the cap beyond it) and exponentials are
+ * float32; distances are float32 differences of positions, exact below 2^24.
+ * Before the product with V each weight is rounded to fp16 (2^-11 of it at most;
+ * once more, where it has become 2^-8 of what it was, when a later page's scores
+ * pass it): with fp16 outputs that adds up to a half to the error of the output's
+ * own rounding, with bf16 ones it does not show. lse and vq_paged_weights never see
+ * it. Positions of a sequence lie within 2^31 of each other. */
 vq_status vq_paged_attention(const vq_paged_desc* desc, const vq_paged_cache* cache, const vq_paged_query* query,
                              void* out, const int64_t out_strides[3], float* lse, void* workspace,
                              size_t workspace_bytes, void* stream);

@@ -267,3 +267,28 @@ def test_a_lower_bound_without_a_causal_mask_hides_nothing_behind(n, G, pos):
     p.fill([320, max(n, 131)])
     first = p.g.integers(0, 320, (2, n)).astype(np.int32)
     p.attend(_q(p, 2 * G, n, torch.bfloat16, 2.0), 0.125, first=first)
+
+
+@pytest.mark.parametrize("n", [1, 20, 150])
+def test_queries_with_one_channel_far_above_the_others(n, monkeypatch):
+    """bf16 query rows with a channel 2^30 above the others: what lies 2^-24 and more below a row's largest magnitude is
+    exact only to 2^-32 of that magnitude (half of fp16's smallest step under the row's power of two)."""
+    p = Paged(1, 2, 64, "int8", 4, seed=n)
+    p.fill([250])
+    for j in range(4):
+        page = p.o["k"][p.table[0, j]]
+        page[..., 0] = po.encode(np.where(p.g.random(page.shape[:-1]) < 0.5, 0.0, 1.0), "int8")
+    p.push()
+    scores = po.scores
+
+    def with_the_rounding_of_queries(c, table, b, h, hq, length, q, sigma, **kw):
+        z, err = scores(c, table, b, h, hq, length, q, sigma, **kw)
+        k = np.abs(po.read(c, table, b, h, 0, length)[0].astype(np.float64))
+        return z, err + sigma * np.abs(q).max(1, keepdims=True) * 2.0 ** -32 * k.sum(1)[None]
+
+    monkeypatch.setattr(po, "scores", with_the_rounding_of_queries)
+    for up in (20, 23, 30):
+        q = _q(p, 4, n, torch.bfloat16)
+        q[..., 0] = 2.0 ** up
+        p.attend(q, 2.0 ** -up)
+        p.attend(q, 2.0 ** -max(up - 8, 0) * 0.01)
