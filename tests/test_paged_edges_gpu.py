@@ -292,3 +292,57 @@ def test_queries_with_one_channel_far_above_the_others(n, monkeypatch):
         q[..., 0] = 2.0 ** up
         p.attend(q, 2.0 ** -up)
         p.attend(q, 2.0 ** -max(up - 8, 0) * 0.01)
+
+
+def test_evict_more_tokens_than_shared_memory_has_keys_for():
+    """Sequences of more than 49152 tokens: the later keys are gathered again for every digit."""
+    L, keep, H = 49152 + 3000, 20000, 2
+    pages = -(-L // 64)
+    for kind in ("distinct", "ties"):
+        p = Paged(2, H, 64, "int8", pages, seed=2, pos=False)
+        p.lens = np.array([L, 49153], np.int32)
+        w = p.o["weight"]
+        w[...] = p.g.gamma(0.1, size=w.shape) if kind == "distinct" else p.g.choice(np.array([0.0, 0.5, 2.0], np.float32), w.shape)
+        for n in ("k_scale", "v_scale"):
+            p.o[n][...] = 0.5
+        p.push()
+        to = Paged(2, H, 64, "int8", -(-keep // 64), seed=3)
+        kept, to_lens = torch.zeros((2, H, keep), dtype=torch.int32, device="cuda"), torch.zeros(2, dtype=torch.int32, device="cuda")
+        vq.vq_paged_evict(p.desc, p.cache, p.dtable, p.dev(p.lens), to.desc, to.cache, to.dtable, to_lens, keep, sinks=5,
+                          recent=100, kept=kept)
+        torch.cuda.synchronize()
+        assert vq.vq_poll_device_error() == 0 and to_lens.tolist() == [keep, keep]
+        for b in range(2):
+            n = int(p.lens[b])
+            for h in range(H):
+                flat = w[p.table[b], h].reshape(-1)[:n].astype(np.float64)
+                flat[:5] = flat[n - 100:] = np.inf
+                want = np.sort(np.lexsort((np.arange(n), -flat))[:keep])
+                assert np.array_equal(kept[b, h].cpu().numpy(), want)
+                at = to.table[b][np.arange(keep) // 64]
+                got = to.cache.weight[torch.from_numpy(at).cuda().long(), h, torch.arange(keep, device="cuda") % 64].cpu().numpy()
+                assert np.array_equal(got, w[p.table[b][want // 64], h, want % 64])
+
+
+def test_two_calls_at_once_on_streams_that_waited():
+    """Two calls that run together, each on a stream that waits for its inputs and for the outputs' first contents."""
+    p = Paged(2, 4, 128, "int8", 64, seed=17)
+    p.fill([4096, 2000])
+    lens = p.dev(p.lens)
+    qs = [_q(p, 16, n, torch.bfloat16) for n in (1, 3, 40)]
+    want = []
+    for q in qs:
+        out = torch.zeros_like(q)
+        vq.vq_paged_attention(p.desc, p.cache, p.dtable, lens, q, 0.1, out)
+        want.append(out)
+    outs = [[torch.zeros_like(q) for _ in range(10)] for q in qs]
+    streams = [torch.cuda.Stream() for _ in qs]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for i in range(10):
+        for s, q, o in zip(streams, qs, outs):
+            vq.vq_paged_attention(p.desc, p.cache, p.dtable, lens, q, 0.1, o[i], stream=s)
+    torch.cuda.synchronize()
+    assert vq.vq_poll_device_error() == 0
+    for w, o in zip(want, outs):
+        assert all(torch.equal(w, x) for x in o)
