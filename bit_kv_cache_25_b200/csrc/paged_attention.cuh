@@ -9,12 +9,11 @@
 // Codes are exact in fp16, and so are fp16 queries. A row of bf16 queries is taken
 // to fp16 after a power of two that puts its largest magnitude in [2^7, 2^8): exact
 // down to 2^-24 of that magnitude, and off by 2^-32 of it at most below (half of
-// fp16's smallest step, 2^-25, over 2^7), which is less than float32 sums of the row
-// lose. Products of q . code are exact and sums are fp32; a page's scales are factors
-// of its scores and of its share of the output, both in fp32. The only other rounding
-// to fewer bits is that of the weights to fp16 before the product with V: 2^-11 of
-// each weight at most, where the output's own rounding is 2^-8 (bf16) or 2^-11 (fp16)
-// of the sum. Log-sum-exp and sums of weights never see it.
+// fp16's smallest step, 2^-25, over 2^7). Products of q . code are exact and sums are
+// fp32; a page's scales are factors of its scores and of its share of the output, both
+// in fp32. The only other rounding to fewer bits is that of the weights to fp16 before
+// the product with V: 2^-11 of each weight at most, where the output's own rounding is
+// 2^-8 (bf16) or 2^-11 (fp16) of the sum. Log-sum-exp and sums of weights never see it.
 #pragma once
 
 #include <cuda_runtime.h>

@@ -346,3 +346,41 @@ def test_two_calls_at_once_on_streams_that_waited():
     assert vq.vq_poll_device_error() == 0
     for w, o in zip(want, outs):
         assert all(torch.equal(w, x) for x in o)
+
+
+@pytest.mark.parametrize("n", [1, 20, 60, 150])
+def test_queries_of_broadcast_heads_and_sequences_without_tokens(n):
+    """Query views whose batch and head strides are 0, a sequence of no token, negative slopes."""
+    p = Paged(3, 2, 128, "e4m3", 3, seed=n)
+    p.fill([192, 0, 77])
+    x = _q(p, 1, n, torch.float16)[:1]
+    p.attend(x.expand(3, 6, n, 128), 0.09)
+    p.attend(x.expand(3, 6, n, 128), 0.09, causal=True, slopes=-2.0 ** -np.arange(4, 10))
+
+
+def test_captured_without_a_workspace():
+    """Graphs whose calls take their workspace from the allocator, replayed in turn and between other allocations."""
+    p = Paged(2, 2, 128, "int8", 100, seed=31)
+    p.fill([6400, 3001])
+    lens = p.dev(p.lens)
+    graphs = []
+    for n in (1, 6, 40):
+        q = _q(p, 4, n, torch.bfloat16)
+        assert vq.vq_paged_attention_workspace(p.desc, 2, 4, n) > 0
+        want, out = torch.zeros_like(q), torch.zeros_like(q)
+        vq.vq_paged_attention(p.desc, p.cache, p.dtable, lens, q, 0.1, want, causal=True)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            vq.vq_paged_attention(p.desc, p.cache, p.dtable, lens, q, 0.1, out, causal=True)
+            vq.vq_paged_attention(p.desc, p.cache, p.dtable, lens, q, 0.1, out, causal=True)
+        graphs.append((g, q, want, out))  # (q stays alive: the graph reads it)
+    for _ in range(3):
+        for g, _, want, out in graphs:
+            out.fill_(7.0)
+            junk = torch.full((1 << 22,), 9.0, device="cuda")
+            g.replay()
+            junk = junk + 1
+            torch.cuda.synchronize()
+            assert torch.equal(out, want)
+    assert vq.vq_poll_device_error() == 0
+    del graphs
