@@ -288,8 +288,8 @@ struct FewRowsView {
         int l, u;
         row_interval(p, sv, r, by_pos, l, u);
         hi_max = max(hi_max, u);
-        hi_min = min(hi_min, u);
-        lo_max = max(lo_max, l);
+        hi_min = min(hi_min, by_pos ? INT32_MAX : u);
+        lo_max = max(lo_max, l);  // (0 where positions decide)
         if (r.hi >= 0) {
           lo_min = min(lo_min, l);
           if (by_pos && p.causal && p.prefix) hi_max = sv.len;
@@ -299,10 +299,12 @@ struct FewRowsView {
         lo[half][e] = l;
         hi[half][e] = by_pos ? INT32_MAX : u;
       }
+    // (unconditional, all four: with the last two in a choice by by_pos, the 16-row kernels for positions and slopes were
+    // compiled to ones that masked no slot at all)
     hi_max = __reduce_max_sync(0xffffffffu, hi_max);
-    hi_min = by_pos ? INT32_MAX : __reduce_min_sync(0xffffffffu, hi_min);
+    hi_min = __reduce_min_sync(0xffffffffu, hi_min);
     lo_min = __reduce_min_sync(0xffffffffu, lo_min);
-    lo_max = by_pos ? 0 : __reduce_max_sync(0xffffffffu, lo_max);
+    lo_max = __reduce_max_sync(0xffffffffu, lo_max);
   }
 };
 

@@ -384,3 +384,22 @@ def test_captured_without_a_workspace():
             assert torch.equal(out, want)
     assert vq.vq_poll_device_error() == 0
     del graphs
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("n,G", [(1, 1), (4, 2), (9, 1), (16, 1), (6, 2), (2, 5), (16, 3), (64, 1), (70, 2)])
+def test_a_distance_bias_by_positions_under_masks_by_slots(n, G, fmt, D, dtype, causal):
+    """Positions with gaps for the bias, and no mask that needs them; what lies behind the last token is not seen."""
+    p = Paged(2, 2, D, fmt, 3, seed=n)
+    p.fill([max(n, 36), max(n, 131)])
+    for b in range(2):
+        for h in range(2):
+            run = np.cumsum(p.g.integers(1, 4, 192))
+            for j in range(3):
+                p.o["pos"][p.table[b, j], h] = run[64 * j:64 * j + 64]
+    p.push()
+    for slopes, cap in ((2.0 ** -np.linspace(3, 9, 2 * G), 0.0), (-2.0 ** -np.linspace(3, 9, 2 * G), 5.0)):
+        p.attend(_q(p, 2 * G, n, dtype), 0.1, causal=causal, slopes=slopes, q_pos=[100, 400], softcap=cap)
