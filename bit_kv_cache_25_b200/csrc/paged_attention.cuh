@@ -70,14 +70,16 @@ __device__ __forceinline__ void mma_16816_from_zero(float (&d)[4], const uint32_
 
 // cap * tanh(z / cap), times log2 e, of z = a * f: its error is a few 2^-24 of the smaller of |z| and the cap, so that a
 // large cap is close to none. Two forms:
-// |z| <= cap / 4: tanh(x) = x * P(x^2), P of degree 2 interpolated at the Chebyshev nodes of [0, 1/16] (4.2e-07 of itself
-// off at most). Most scores are small enough for it, and it takes two multiply-adds where the other takes two turns of the
-// exponential unit: a warp decides for all of its values.
+// |z| <= cap / 4: tanh(x) = x * P(x^2), P of degree 3 interpolated at the Chebyshev nodes of [0, 1/16] (2.5e-09 of itself
+// off at most, below float32's own rounding; degree 2 would be 4.0e-07 off, which shows in the weights). Most scores are
+// small enough for it, and it takes three multiply-adds where the other takes two turns of the exponential unit: a warp
+// decides for all of its values.
 constexpr float kCapSmall = 0.25f;
 __device__ __forceinline__ float capped_small(float a, float f_over_cap, float cap_log2e) {
   const float x = a * f_over_cap, y = x * x;
-  const float t = fmaf(fmaf(0.1284143328666687f * cap_log2e, y, -0.3332189619541168f * cap_log2e), y, 0.9999995827674866f * cap_log2e);
-  return x * t;
+  float t = fmaf(-0.05132700516785341f * cap_log2e, y, 0.13323126058764362f * cap_log2e);
+  t = fmaf(t, y, -0.33333206285536826f * cap_log2e);
+  return x * fmaf(t, y, 0.9999999975205603f * cap_log2e);
 }
 // Any z, where a warp has larger ones: beyond cap / 4 tanh(x) = 1 - 2 / (e^2x + 1), which saturates without a NaN at both
 // ends (and cancels below: its error is a few 2^-24 of the cap).

@@ -27,7 +27,8 @@
 // and 128 keys takes about 5050 cycles; its products take 2240 and its exponentials 2050.
 // What sets it is each query tile's chain (scores, softmax, P V, the next scores: P lies
 // over S, for which tensor memory has no second place at head_dim 128). A unit of 128 rows
-// would unpack K and V twice as often.
+// would unpack K and V twice as often. (Its 512 items are 3.46 waves of the 148 SMs and run as
+// 4: 13 % of the SMs' time is idle.)
 #pragma once
 
 #include <cuda_runtime.h>

@@ -339,13 +339,15 @@ vq_status vq_paged_attention_workspace(const vq_paged_desc* desc, int32_t batch,
  * Arithmetic: codes and fp16 queries are exact operands; a row of bf16 queries is
  * taken to fp16 times a power of two, exactly down to 2^-24 of the row's largest
  * magnitude and within 2^-32 of that magnitude below it. Products, sums, scales,
- * caps (within 2^-21 of the score, or of the cap beyond it) and exponentials are
+ * caps (within 2^-21 of a score up to cap / 4, of the cap beyond) and exponentials are
  * float32; distances are float32 differences of positions, exact below 2^24.
- * Before the product with V each weight is rounded to fp16 (2^-11 of it at most;
- * once more, where it has become 2^-8 of what it was, when a later page's scores
- * pass it): with fp16 outputs that adds up to a half to the error of the output's
- * own rounding, with bf16 ones it does not show. lse and vq_paged_weights never see
- * it. Positions of a sequence lie within 2^31 of each other. */
+ * Before the product with V each weight is rounded to fp16, by 2^-11 of it at most
+ * or by 2^-32 of the row's largest one, whichever is more (with more than 48 rows
+ * per key head, of weight times the page's V scale; once more, where it has become
+ * 2^-8 of what it was, when a later page's scores pass it): with fp16 outputs that
+ * adds up to a half to the error of the output's own rounding, with bf16 ones it
+ * does not show. lse and vq_paged_weights never see it. Positions of a sequence lie
+ * within 2^31 of each other. */
 vq_status vq_paged_attention(const vq_paged_desc* desc, const vq_paged_cache* cache, const vq_paged_query* query,
                              void* out, const int64_t out_strides[3], float* lse, void* workspace,
                              size_t workspace_bytes, void* stream);

@@ -137,7 +137,8 @@ def scores(c, table, b, h, hq, length, q, sigma, *, q_len, q_pos=None, prefix=0,
     z = raw
     if cap > 0:
         z = cap * np.tanh(raw / cap)
-        err = err + np.minimum(cap * 2.0 ** -21, np.abs(raw) * 2.0 ** -19)
+        # small scores by a polynomial (eight float32 roundings of the score), larger ones by exponentials (of the cap)
+        err = err + np.where(np.abs(raw) <= 0.2499 * cap, np.abs(raw), cap) * 2.0 ** -21
     slot = np.arange(length)
     kp = per_slot(c, "pos", table, b, h, length) if c["pos"] is not None else slot
     own = length - q_len + np.arange(q_len)
