@@ -17,8 +17,9 @@ struct PagedPlan {
 constexpr int kAlonePages = 32;
 // At most so many rows per key head take the few-row kernels, which read the codes once per 8 or 16 rows; above, the
 // tensor cores' tiles of 256 rows win. Few-row against many-row kernel, 8192 tokens, head_dim 128, int8: 8 sequences of
-// 8 heads, 32 rows 94 against 122 us, 48 rows 114 against 124, 64 rows 143 against 125; one sequence, 48 rows 37 against
-// 32 us; 32 sequences, 48 rows 345 against 430 us. The weights: 84 against 110, 29 against 20, 233 against 403 us at 48.
+// 8 heads, 32 rows 92 against 125 us, 48 rows 127 against 127, 64 rows 152 against 127; one sequence, 48 rows 35 against
+// 31 us; 32 sequences, 48 rows 371 against 440 us, 64 rows 471 against 436. The weights at 48 rows: 86 against 121, 29
+// against 22, 229 against 440 us.
 constexpr int kFewRows = 48;
 
 inline PagedPlan paged_plan(int B, int H, int G, int n, int max_pages, int sms) {
