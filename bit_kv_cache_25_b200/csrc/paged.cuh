@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const __gr
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         xv[j] = V::get(val[i], 4 * g + j);
-        if (rare) xv[j] = cut && xv[j] == xv[j] ? fminf(fmaxf(xv[j], -kPagedMost), kPagedMost) : 0.0f;
+        if (rare) xv[j] = scale > 0.0f && xv[j] == xv[j] ? fminf(fmaxf(xv[j], -kPagedMost), kPagedMost) : 0.0f;
       }
       if (CODE == kCodeInt8) {
         // x * inv rounded by 1.5 * 2^23, then checked: x - k * scale is exact here, so a

@@ -403,3 +403,18 @@ def test_a_distance_bias_by_positions_under_masks_by_slots(n, G, fmt, D, dtype, 
     p.push()
     for slopes, cap in ((2.0 ** -np.linspace(3, 9, 2 * G), 0.0), (-2.0 ** -np.linspace(3, 9, 2 * G), 5.0)):
         p.attend(_q(p, 2 * G, n, dtype), 0.1, causal=causal, slopes=slopes, q_pos=[100, 400], softcap=cap)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+def test_append_of_signed_zeros_and_nan_alone(fmt, dtype):
+    """Nothing but zeros of both signs and NaN: a scale of 0 and codes of +0, also when later tokens bring values."""
+    p = Paged(1, 2, 64, fmt, 2, seed=2)
+    x = torch.zeros((1, 2, 9, 64), device="cuda", dtype=dtype)
+    x[..., ::2] = -0.0
+    x[:, :, 3, 5] = float("nan")
+    p.append(x, -x)
+    p.check()
+    p.append(*p.tokens(3, dtype))
+    p.append(x, -x)
+    p.check()
